@@ -303,6 +303,99 @@ PIVOT_API pivot_status pivot_decode_rowselect(const uint32_t *keys, const int32_
                                               const int64_t *plen_offsets_dev, int B, int k, int c, int g,
                                               int32_t *indices, float *scores_opt, pivot_stream_t stream);
 
+/* ---- A paged key/value cache in 8 bits, and attention over it.
+ *
+ * The rows that the indexer selects (Eq. 1, 6, 9) name the cached tokens a query attends to.  These calls keep
+ * those tokens and read them:
+ *   pivot_kv_append              writes a step's new keys and values, rotated by position, into the cache;
+ *   pivot_kv_attention           attends to all cached tokens (the guardrail's dense side), or to the last
+ *                                `window` tokens and the first `sinks`;
+ *   pivot_kv_attention_selected  attends to each row's own list of positions, as pivot_reuse_varlen /
+ *                                pivot_refine_varlen (and their prefill forms) return it.
+ *
+ * The cache holds a key as k = payload * 2^e: payload an OCP e4m3 byte, e one int8 exponent for each block of
+ * PIVOT_KV_BLOCK tokens and head; values likewise.  k, v [num_pages, kv_heads, page_size, d] bytes; k_exp, v_exp
+ * [num_pages, kv_heads, page_size / PIVOT_KV_BLOCK].  kv_heads >= 1; page_size a positive multiple of
+ * PIVOT_KV_BLOCK; d = 64 or 128; k and v 16-byte aligned; num_pages * kv_heads * page_size < 2^31.  An exponent
+ * outside [-60, 60] is never written; what reads one outside that range gives is undefined (and faults nothing).
+ *
+ * A step: B sequences.  Sequence b holds lens[b] tokens, this step's included, and owns the rows
+ * row_offsets[b] .. row_offsets[b+1] - 1 of the row tensors: its last tokens, so that with n_b rows row i is the
+ * position p = lens[b] - n_b + i.  row_offsets [B+1] starts at 0 and does not decrease.  Position s lies in page
+ * block_table[b, s / page_size] at slot s % page_size.  A table entry outside [0, num_pages), or past the table's
+ * width, means that the position is absent: it is not written, and no row sees it.  A row with p < 0, and a row
+ * behind row_offsets[B], belongs to no token: nothing is appended for it; attention gives zeros (lse = -inf) for
+ * the former and leaves the latter's outputs as they were.  All of this is read on the device, so a captured
+ * call follows the tensors' current contents.
+ *
+ * All pointers inside the two structs are device pointers; the structs themselves are read on the host during
+ * the call.  Rows of q, k and v are `*_stride` elements apart (heads contiguous: head h of a row starts at h * d),
+ * so that slices of one fused projection are taken as they are.  Row starts must be 16-byte aligned. */
+#define PIVOT_KV_BLOCK 16
+#define PIVOT_KV_EXP_MIN (-60)
+#define PIVOT_KV_EXP_MAX 60
+
+typedef struct {
+  void *k, *v;            /* e4m3 payload */
+  int8_t *k_exp, *v_exp;  /* exponents of the blocks' scales */
+  int32_t num_pages, kv_heads, page_size, d;
+} pivot_kv_cache;
+
+typedef struct {
+  const int32_t *block_table;   /* [B, table_width], rows table_stride entries apart */
+  const int64_t *row_offsets;   /* [B+1] */
+  const int64_t *lens;          /* [B] */
+  int64_t table_stride, rows;   /* rows: of the row tensors (row_offsets[B] may be less) */
+  int32_t table_width, B;
+} pivot_kv_step;
+
+/* Appends a step's k and v [rows, kv_heads, d] (bf16 or fp32).  Where cos and sin [n_pos, rot / 2] (fp32) are
+ * given, the first `rot` dims of each key are rotated by the row's position: pairs (x1, x2) = dims (i, i + rot/2),
+ * or (2i, 2i + 1) with `interleaved`, become (x1 cos - x2 sin, x2 cos + x1 sin).  rot is a multiple of 16, at
+ * most d (0: no rotation, cos and sin NULL); n_pos >= table_width * page_size; cos and sin 16-byte aligned.
+ * q [rows, q_heads, d] (optional) is rotated the same way into q_out [rows, q_heads, d] (dt), which may be q
+ * itself (then with the same stride).
+ *
+ * The scale of a block whose first token of the sequence is new: the least e in [PIVOT_KV_EXP_MIN,
+ * PIVOT_KV_EXP_MAX] with |y| <= 448 * 2^e for the finite values y of its new tokens and head.  A block that
+ * already holds earlier tokens of the sequence takes the larger of that and its present exponent; where it rises,
+ * the earlier payload is rounded again to the new scale (exact, but for values that fall below e4m3's normal
+ * range).  payload = e4m3(y * 2^-e), to nearest even; NaN stays NaN, larger values and infinities become
+ * +-448.  Nothing else of the cache is written.  Two sequences may share a page only where neither appends to it.
+ * fp32 arithmetic (the rotation's products and one sum); an exponent is exact: a largest value within rounding of
+ * a step between two exponents is computed again in 64 bits.
+ * Errors: PIVOT_ERR_INVALID_ARG, PIVOT_ERR_UNSUPPORTED_SHAPE, PIVOT_ERR_CUDA. */
+PIVOT_API pivot_status pivot_kv_append(const pivot_kv_cache *cache, const pivot_kv_step *step, const void *k,
+                                       int64_t k_stride, const void *v, int64_t v_stride, pivot_dtype dt,
+                                       const float *cos, const float *sin, int64_t n_pos, int rot, int interleaved,
+                                       const void *q, int64_t q_stride, int q_heads, void *q_out,
+                                       int64_t q_out_stride, pivot_stream_t stream);
+
+/* out[r, j] = sum_s p_s v_s / sum_s p_s with p_s = exp(scale * q[r, j] . k_s) over the tokens s that row r sees,
+ * of key head j / (q_heads / kv_heads); lse_opt[r, j] = ln sum_s p_s (q_heads a multiple of kv_heads).  The row at
+ * position p sees the present positions 0 <= s <= p; with window > 0 only those with s > p - window or s < sinks.
+ * q [rows, q_heads, d] and out [rows, q_heads, d] (contiguous) of dt, lse_opt [rows, q_heads] fp32 or NULL.  A row
+ * that sees nothing gives zeros and lse -inf.  What absent or masked positions hold, NaN included, changes nothing.
+ * Scores, softmax statistics and output sums are fp32.  bf16: the weights p enter the output product with 8 bits
+ * or more; fp32: with 21 or more.
+ * ws: pivot_kv_workspace_size bytes on the current device (256-byte aligned; 0: the call would be refused), with
+ * topk 0 for pivot_kv_attention. */
+PIVOT_API size_t pivot_kv_workspace_size(int64_t rows, int B, int q_heads, int kv_heads, int d, int topk,
+                                         pivot_dtype dt);
+PIVOT_API pivot_status pivot_kv_attention(const pivot_kv_cache *cache, const pivot_kv_step *step, const void *q,
+                                          int64_t q_stride, int q_heads, pivot_dtype dt, float scale, int64_t window,
+                                          int64_t sinks, void *out, float *lse_opt, void *ws, size_t ws_bytes,
+                                          pivot_stream_t stream);
+
+/* As pivot_kv_attention, over the entries s of indices[r, 0 .. topk) with 0 <= s <= p that are present, in any
+ * order; an entry that is listed twice counts twice.  Rows of indices are index_stride entries apart.  The
+ * indexer's rows, its candidate sets' rows and -1 padding are all taken as they are. */
+PIVOT_API pivot_status pivot_kv_attention_selected(const pivot_kv_cache *cache, const pivot_kv_step *step,
+                                                   const void *q, int64_t q_stride, int q_heads, pivot_dtype dt,
+                                                   float scale, const int32_t *indices, int64_t index_stride,
+                                                   int topk, void *out, float *lse_opt, void *ws, size_t ws_bytes,
+                                                   pivot_stream_t stream);
+
 /* Synchronises `stream`, then reads the device status word that the last
  * call using workspace `ws` left: PIVOT_OK, PIVOT_ERR_DEVICE_TIMEOUT or
  * PIVOT_ERR_DEVICE_BOUNDS (or PIVOT_ERR_CUDA if the sync/copy failed). */

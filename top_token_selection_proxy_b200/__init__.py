@@ -47,10 +47,27 @@ EXPORTS = (
     "pivot_decode_shard_workspace_size", "pivot_decode_shard_select", "pivot_decode_merge_workspace_size",
     "pivot_decode_merge",
     "pivot_decode_shard_rescore", "pivot_decode_rowselect",
+    "pivot_kv_append", "pivot_kv_workspace_size", "pivot_kv_attention", "pivot_kv_attention_selected",
 )
 
 # proxy aggregation (PIVOT paper, Ablation Studies, Proxy aggregation, Table 2)
 AGGREGATION = {"mean": 0, "first": 1, "last": 2}
+
+
+# the paged key/value cache (pivot.h: PIVOT_KV_BLOCK): tokens under one scale
+KV_BLOCK = 16
+
+
+class _CacheC(ctypes.Structure):  # pivot_kv_cache
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("d", ctypes.c_int32)]
+
+
+class _StepC(ctypes.Structure):  # pivot_kv_step
+    _fields_ = [("block_table", ctypes.c_void_p), ("row_offsets", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("rows", ctypes.c_int64), ("table_width", ctypes.c_int32),
+                ("B", ctypes.c_int32)]
 
 
 class PivotError(RuntimeError):
@@ -101,6 +118,14 @@ def lib() -> ctypes.CDLL:
         L.pivot_decode_merge.argtypes = [I, P, I, P, P, I, I, I, I, P, P, P, P, P, P, P, P, SZ, P]
         L.pivot_decode_shard_rescore.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, P, P, P, SZ, P]
         L.pivot_decode_rowselect.argtypes = [P, P, P, I, I, I, I, P, P, P]
+        F = ctypes.c_float
+        L.pivot_kv_append.argtypes = [P, P, P, I64, P, I64, I, P, P, I64, I, I, P, I64, I, P, I64, P]
+        L.pivot_kv_workspace_size.argtypes = [I64, I, I, I, I, I, I]
+        L.pivot_kv_workspace_size.restype = SZ
+        L.pivot_kv_attention.argtypes = [P, P, P, I64, I, I, F, I64, I64, P, P, P, SZ, P]
+        L.pivot_kv_attention_selected.argtypes = [P, P, P, I64, I, I, F, P, I64, I, P, P, P, SZ, P]
+        for f in ("pivot_kv_append", "pivot_kv_attention", "pivot_kv_attention_selected"):
+            getattr(L, f).restype = I
         for f in ("pivot_decode_shard_select", "pivot_decode_merge", "pivot_decode_shard_rescore",
                   "pivot_decode_rowselect"):
             getattr(L, f).restype = I
@@ -562,6 +587,219 @@ def decode_rowselect(keys, cand, plen_offsets, topk: int, c: int, g: int, *, sco
     return idx, sc
 
 
+# ---------------------------------------------------------------- the paged 8-bit key/value cache
+
+
+class KVCache:
+    """A paged cache of keys and values in 8 bits (pivot_kv_cache).
+
+    k, v: float8_e4m3fn [num_pages, kv_heads, page_size, d] (d = 64 or 128); k_exp, v_exp: int8
+    [num_pages, kv_heads, page_size / KV_BLOCK].  A key is payload * 2**k_exp of its block of KV_BLOCK
+    tokens and head.  The tensors are the caller's, contiguous and on one device; the cache keeps
+    references to them and the calls below write them in place.  ``KVCache.empty`` allocates them."""
+
+    def __init__(self, k, v, k_exp, v_exp):
+        if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
+            raise ValueError("k and v must be float8_e4m3fn [num_pages, kv_heads, page_size, d]")
+        pages, heads, page, d = k.shape
+        if page % KV_BLOCK or page == 0:
+            raise ValueError(f"page_size must be a positive multiple of {KV_BLOCK}, got {page}")
+        if v.shape != k.shape or k_exp.shape != (pages, heads, page // KV_BLOCK) or v_exp.shape != k_exp.shape:
+            raise ValueError("shape mismatch between k, v, k_exp and v_exp")
+        if k_exp.dtype != torch.int8 or v_exp.dtype != torch.int8:
+            raise ValueError("k_exp and v_exp must be int8")
+        _need_cuda(k, v, k_exp, v_exp)
+        if len({t.device for t in (k, v, k_exp, v_exp)}) != 1:
+            raise ValueError("k, v, k_exp and v_exp must be on one device")
+        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
+        self.device, self.num_pages, self.kv_heads, self.page_size, self.d = k.device, pages, heads, page, d
+        self._c = _CacheC(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, heads, page, d)
+
+    @classmethod
+    def empty(cls, num_pages: int, kv_heads: int, page_size: int, d: int, device="cuda") -> "KVCache":
+        """A cache of zeros."""
+        shape = (num_pages, kv_heads, page_size, d)
+        exps = (num_pages, kv_heads, page_size // KV_BLOCK)
+        return cls(*(torch.zeros(shape, dtype=torch.float8_e4m3fn, device=device) for _ in range(2)),
+                   *(torch.zeros(exps, dtype=torch.int8, device=device) for _ in range(2)))
+
+
+class _On:
+    """The call's device made current, and its stream (the device's current one unless given)."""
+
+    def __init__(self, device, stream):
+        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+        self.stream, self.device = stream, device
+
+    def __enter__(self):
+        if self.guard is not None:
+            self.guard.__enter__()
+        if self.stream is None:
+            self.stream = torch.cuda.current_stream(self.device)
+        elif self.stream.device != self.device:
+            self.__exit__(None, None, None)
+            raise ValueError(f"the stream is of {self.stream.device}, the cache is on {self.device}")
+        return self
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+    def new(self, shape, dtype):
+        """A tensor that belongs to the call's stream."""
+        if self.stream == torch.cuda.current_stream(self.device):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        with torch.cuda.stream(self.stream):
+            return torch.empty(shape, dtype=dtype, device=self.device)
+
+
+def _kv_rows(name, t, heads, cache, dtype=None):
+    """Checks a row tensor [rows, heads, d] whose rows may be slices of a wider one."""
+    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != cache.d or (heads and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [rows, {heads or 'heads'}, {cache.d}]")
+    _dt(t)
+    if t.device != cache.device or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{name} must be on {cache.device}, of the same type as the other rows")
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != cache.d):
+        raise ValueError(f"{name}: each row's heads must be contiguous")
+
+
+def _row_stride(t):
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+
+
+def _kv_step(cache, block_table, row_offsets, lens, rows, stream):
+    """The step's C struct, and what it points to."""
+    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != cache.device or \
+            block_table.shape[1] == 0 or block_table.stride(1) != 1:
+        raise ValueError(f"block_table must be an int32 [B, width] tensor on {cache.device}, its rows contiguous")
+    B, width = block_table.shape
+    off = _positions_dev(row_offsets, cache.device, stream)
+    n = _positions_dev(lens, cache.device, stream)
+    for t, m, name in ((off, B + 1, "row_offsets"), (n, B, "lens")):
+        if t.dtype != torch.int64 or t.shape != (m,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be {m} contiguous int64 values")
+    step = _StepC(block_table.data_ptr(), off.data_ptr(), n.data_ptr(),
+                  block_table.stride(0) if B > 1 else max(block_table.stride(0), width), rows, width, B)
+    return step, (off, n)
+
+
+def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None, sin=None, interleaved: bool = False,
+              q=None, q_out=None, stream=None):
+    """Writes a step's keys and values into the cache (pivot_kv_append); returns the rotated q, or None.
+
+    k, v [rows, kv_heads, d] (bf16 or fp32; rows may be slices of a wider tensor).  Sequence b owns rows
+    row_offsets[b] .. row_offsets[b+1]-1, the last of its lens[b] tokens (this step's included), and its
+    position s lies in page block_table[b, s // page_size].  row_offsets [B+1] and lens [B]: int64 CUDA
+    tensors, DeviceOffsets, or host values (copied on every call).  cos, sin [positions, rot / 2] fp32
+    rotate the first rot dims of k, and of q [rows, heads, d] into q_out (a new tensor unless given; q
+    itself is allowed): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no
+    token leave cache and q_out as they were."""
+    _kv_rows("k", k, cache.kv_heads, cache)
+    _kv_rows("v", v, cache.kv_heads, cache, k.dtype)
+    rows = k.shape[0]
+    if v.shape[0] != rows:
+        raise ValueError("k and v must have the same rows")
+    rot = n_pos = 0
+    if (cos is None) != (sin is None):
+        raise ValueError("cos and sin go together")
+    if cos is not None:
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32 or \
+                cos.device != cache.device or sin.device != cache.device or not cos.is_contiguous() or \
+                not sin.is_contiguous():
+            raise ValueError(f"cos and sin must be contiguous fp32 [positions, rot / 2] tensors on {cache.device}")
+        n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    if q is not None:
+        _kv_rows("q", q, 0, cache, k.dtype)
+        if q.shape[0] != rows:
+            raise ValueError("q must have k's rows")
+        if q_out is not None:
+            _kv_rows("q_out", q_out, q.shape[1], cache, k.dtype)
+            if q_out.shape[0] != rows:
+                raise ValueError("q_out must have q's rows")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    with _On(cache.device, stream) as on:
+        step, _keep = _kv_step(cache, block_table, row_offsets, lens, rows, on.stream)
+        if rows == 0:
+            return q_out if q_out is not None or q is None else q.new_empty(q.shape)
+        if q is not None and q_out is None:
+            q_out = on.new(q.shape, q.dtype)
+        _check(lib().pivot_kv_append(
+            ctypes.byref(cache._c), ctypes.byref(step), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v),
+            _dt(k), _ptr(cos), _ptr(sin), n_pos, rot, int(interleaved), _ptr(q), 0 if q is None else _row_stride(q),
+            0 if q is None else q.shape[1], _ptr(q_out), 0 if q is None else _row_stride(q_out),
+            on.stream.cuda_stream), "pivot_kv_append")
+    return q_out
+
+
+def _kv_attention(where, q, cache, block_table, row_offsets, lens, scale, lse, out, ws, stream, topk, call):
+    _kv_rows("q", q, 0, cache)
+    rows, heads, d = q.shape
+    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or
+                            not out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor of q's shape, type and device")
+    given = isinstance(lse, torch.Tensor)
+    if given and (lse.shape != (rows, heads) or lse.dtype != torch.float32 or lse.device != q.device or
+                  not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [rows, heads] tensor on q's device")
+    with _On(cache.device, stream) as on:
+        step, _keep = _kv_step(cache, block_table, row_offsets, lens, rows, on.stream)
+        if out is None:
+            out = on.new((rows, heads, d), q.dtype)
+        z = lse if given else on.new((rows, heads), torch.float32) if lse else None
+        if rows == 0:
+            return out, z
+        nbytes = int(lib().pivot_kv_workspace_size(rows, step.B, heads, cache.kv_heads, d, topk, _dt(q)))
+        if nbytes == 0:
+            raise PivotError(2, where, "unsupported shape")
+        # scratch of this call alone unless the caller keeps one: calls on two streams, and captured ones, share none
+        w = on.new((nbytes,), torch.uint8) if ws is None else ws.get(nbytes)
+        _check(call(ctypes.byref(cache._c), ctypes.byref(step), q.data_ptr(), _row_stride(q), heads, _dt(q),
+                    d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(z), w.data_ptr(), w.numel(),
+                    on.stream.cuda_stream), where)
+    return out, z
+
+
+def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Optional[float] = None, window: int = 0,
+                 sinks: int = 0, lse=False, out=None, ws: Optional[Workspace] = None, stream=None):
+    """Attention of a step's rows over the cached tokens (pivot_kv_attention).  Returns (out, lse|None).
+
+    q [rows, heads, d] (bf16 or fp32), heads a multiple of the cache's; the step as kv_append takes it,
+    after it.  The row at position p sees the positions s <= p; with ``window`` only s > p - window, and the
+    first ``sinks``.  ``scale`` defaults to d ** -0.5.  ``lse``: False, True, or an fp32 [rows, heads] tensor
+    that receives ln sum exp(scale q.k).  Rows that see nothing give zeros and -inf; rows behind
+    row_offsets[B] are not written (they are undefined in an ``out`` that the call allocates)."""
+
+    def call(c, s, qp, qs, h, dt, sc, o, z, w, wb, st):
+        return lib().pivot_kv_attention(c, s, qp, qs, h, dt, sc, window, sinks, o, z, w, wb, st)
+
+    return _kv_attention("pivot_kv_attention", q, cache, block_table, row_offsets, lens, scale, lse, out, ws, stream,
+                         0, call)
+
+
+def kv_attention_selected(q, cache: KVCache, indices, block_table, row_offsets, lens, *,
+                          scale: Optional[float] = None, lse=False, out=None, ws: Optional[Workspace] = None,
+                          stream=None):
+    """Attention of each row over its own positions (pivot_kv_attention_selected).  Returns (out, lse|None).
+
+    indices int32 [rows, k]: the indexer's rows (reuse, refine, indexer_dense and their batch forms), or any
+    list of positions of the row's sequence; entries below 0 or behind the row's own position count as
+    absent, an entry listed twice counts twice.  The rest as kv_attention."""
+    if indices.dim() != 2 or indices.dtype != torch.int32 or indices.shape[0] != q.shape[0] or \
+            indices.shape[1] == 0 or indices.device != cache.device or indices.stride(1) != 1:
+        raise ValueError(f"indices must be an int32 [rows, k] tensor on {cache.device}, its rows contiguous")
+    topk = indices.shape[1]
+    stride = indices.stride(0) if indices.shape[0] > 1 else max(indices.stride(0), topk)
+
+    def call(c, s, qp, qs, h, dt, sc, o, z, w, wb, st):
+        return lib().pivot_kv_attention_selected(c, s, qp, qs, h, dt, sc, indices.data_ptr(), stride, topk, o, z, w,
+                                                 wb, st)
+
+    return _kv_attention("pivot_kv_attention_selected", q, cache, block_table, row_offsets, lens, scale, lse, out, ws,
+                         stream, topk, call)
+
+
 def last_device_status(ws: Workspace, stream=None) -> int:
     """Synchronise the stream and return the device status code of the last call on ``ws``."""
     return int(lib().pivot_last_device_status(_ptr(ws.buf), _stream(stream)))
@@ -609,6 +847,7 @@ __all__ = [
     "indexer_dense_range", "reuse_range", "refine_range",
     "group_chunks", "refine_host", "refine_streamed",
     "decode_shard_select", "decode_merge", "decode_shard_rescore", "decode_rowselect", "DeviceOffsets",
+    "KVCache", "KV_BLOCK", "kv_append", "kv_attention", "kv_attention_selected",
     "set_device_timeout_ns", "set_debug_flags", "KernelTimer", "OP_DENSE", "OP_REUSE", "OP_REFINE", "BF16", "F32",
     "STATUS",
 ]

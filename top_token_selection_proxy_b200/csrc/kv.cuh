@@ -1,0 +1,90 @@
+// kv.cuh -- what the kernels of the paged 8-bit key/value cache share: the cache and the step as the device sees
+// them, e4m3 conversions and the search for a row's sequence.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "kernels.cuh"
+#include "ptx.cuh"
+
+namespace pivot {
+
+constexpr int kKvBlock = PIVOT_KV_BLOCK;
+
+struct KvCache {
+  uint8_t *k, *v;      // e4m3 [pages, hk, ps, d]
+  int8_t *ke, *ve;     // [pages, hk, ps / 16]
+  int pages, hk, ps, d;
+};
+
+struct KvStep {
+  const int32_t* table;  // [B, width], rows `stride` apart
+  const int64_t* off;    // [B+1]
+  const int64_t* lens;   // [B]
+  int64_t stride, rows;
+  int width, B;
+};
+
+struct KvAppendArgs {
+  KvCache c;
+  KvStep st;
+  const void *k, *v, *q;
+  void* q_out;
+  int64_t k_stride, v_stride, q_stride, q_out_stride;  // elements
+  const float *cos, *sin;  // [n_pos, rot / 2]
+  int64_t n_pos;
+  int rot, interleaved, hq, rows_per_cta;
+  bool is_bf16;
+};
+
+struct KvAttnArgs {
+  KvCache c;
+  KvStep st;
+  const void* q;
+  void* out;
+  float* lse;             // or null
+  int64_t q_stride;
+  int hq, group;          // query heads; query heads of one key head
+  float scale2;           // scale * log2(e): scores in units of log 2
+  int64_t window, sinks;  // window 0: none
+  const int32_t* indices; // selected form: [rows, topk], rows idx_stride apart; else null
+  int64_t idx_stride;
+  int topk;
+  bool is_bf16;
+};
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t s);
+cudaError_t launch_kv_attn_simple(const KvAttnArgs& a, cudaStream_t s);
+
+// The sequence b with off[b] <= r < off[b+1], or -1.
+__device__ __forceinline__ int kv_sequence_of(const KvStep& st, int64_t r) {
+  if (r >= st.off[st.B]) return -1;
+  int lo = 0, hi = st.B;  // off[lo] <= r < off[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (st.off[mid] <= r) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// The page of a position below 2^31, or -1 where it is absent.
+__device__ __forceinline__ int kv_page(const KvStep& st, const KvCache& c, int b, uint32_t pos) {
+  const uint32_t i = pos / (uint32_t)c.ps;
+  if (i >= (uint32_t)st.width) return -1;
+  const int pg = __ldg(st.table + (int64_t)b * st.stride + i);
+  return pg >= 0 && pg < c.pages ? pg : -1;
+}
+
+__device__ __forceinline__ float kv_e4m3_to_f32(uint8_t x) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(x, __NV_E4M3);
+  return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+// 2^e for an integer e in [-126, 127].
+__device__ __forceinline__ float kv_exp2i(int e) { return __int_as_float((e + 127) << 23); }
+
+// A score's scale 2^e of a cache exponent (any int8: below -126 it is 2^-126).
+__device__ __forceinline__ float kv_scale(int e) { return kv_exp2i(max(e, -126)); }
+
+}  // namespace pivot

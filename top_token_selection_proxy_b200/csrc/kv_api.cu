@@ -1,0 +1,176 @@
+// kv_api.cu -- host side of the pivot_kv_* calls of include/pivot.h: argument checks and launches.  Nothing is
+// allocated and no call synchronises the host.
+#include <cmath>
+
+#include "kv.cuh"
+
+using namespace pivot;
+
+namespace {
+
+bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+pivot_status check_cache(const pivot_kv_cache* c) {
+  if (!c || !c->k || !c->v || !c->k_exp || !c->v_exp) return PIVOT_ERR_INVALID_ARG;
+  if (c->num_pages <= 0 || c->kv_heads <= 0 || c->page_size <= 0 || c->page_size % PIVOT_KV_BLOCK)
+    return PIVOT_ERR_INVALID_ARG;
+  if (!aligned(c->k, 16) || !aligned(c->v, 16)) return PIVOT_ERR_INVALID_ARG;
+  if (c->d != 64 && c->d != 128) return PIVOT_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)c->num_pages * c->kv_heads >= (int64_t)0x80000000ll / c->page_size) return PIVOT_ERR_UNSUPPORTED_SHAPE;
+  return PIVOT_OK;
+}
+
+pivot_status check_step(const pivot_kv_step* s, const pivot_kv_cache* c) {
+  if (!s || !s->block_table || !s->row_offsets || !s->lens) return PIVOT_ERR_INVALID_ARG;
+  if (s->B <= 0 || s->rows < 0 || s->table_width <= 0 || s->table_stride < s->table_width) return PIVOT_ERR_INVALID_ARG;
+  if (s->rows >= 0x7FFFFFF0ll || (int64_t)s->table_width * c->page_size >= 0x7FFFFFF0ll)
+    return PIVOT_ERR_UNSUPPORTED_SHAPE;
+  return PIVOT_OK;
+}
+
+// Row tensors [rows, heads, d]: rows `stride` elements apart, each on a 16-byte boundary.
+pivot_status check_rows(const void* p, int64_t stride, int64_t heads, int d, pivot_dtype dt) {
+  const int64_t esz = dt == PIVOT_BF16 ? 2 : 4;
+  if (!p || stride < heads * d || !aligned(p, 16) || stride * esz % 16) return PIVOT_ERR_INVALID_ARG;
+  return PIVOT_OK;
+}
+
+KvCache device_cache(const pivot_kv_cache& c) {
+  return {static_cast<uint8_t*>(c.k), static_cast<uint8_t*>(c.v), c.k_exp, c.v_exp, c.num_pages, c.kv_heads,
+          c.page_size, c.d};
+}
+
+KvStep device_step(const pivot_kv_step& s) {
+  return {s.block_table, s.row_offsets, s.lens, s.table_stride, s.rows, s.table_width, s.B};
+}
+
+int sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n <= 0)
+    return 148;
+  return n;
+}
+
+// Checks that the attention calls share, and the argument block they launch with.
+pivot_status attention_args(const pivot_kv_cache* cache, const pivot_kv_step* step, const void* q, int64_t q_stride,
+                            int q_heads, pivot_dtype dt, float scale, void* out, void* ws, KvAttnArgs* a) {
+  pivot_status st = check_cache(cache);
+  if (st == PIVOT_OK) st = check_step(step, cache);
+  if (st != PIVOT_OK) return st;
+  if (dt != PIVOT_BF16 && dt != PIVOT_F32) return PIVOT_ERR_INVALID_ARG;
+  if (q_heads <= 0 || q_heads % cache->kv_heads || !out || !aligned(out, 16) || !ws || !aligned(ws, 256) ||
+      !std::isfinite(scale))
+    return PIVOT_ERR_INVALID_ARG;
+  st = check_rows(q, q_stride, q_heads, cache->d, dt);
+  if (st != PIVOT_OK) return st;
+  if (q_heads > 1024) return PIVOT_ERR_UNSUPPORTED_SHAPE;
+  a->c = device_cache(*cache);
+  a->st = device_step(*step);
+  a->q = q;
+  a->out = out;
+  a->q_stride = q_stride;
+  a->hq = q_heads;
+  a->group = q_heads / cache->kv_heads;
+  a->scale2 = scale * 1.4426950408889634f;
+  a->is_bf16 = dt == PIVOT_BF16;
+  return PIVOT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+pivot_status pivot_kv_append(const pivot_kv_cache* cache, const pivot_kv_step* step, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, pivot_dtype dt, const float* cos, const float* sin,
+                             int64_t n_pos, int rot, int interleaved, const void* q, int64_t q_stride, int q_heads,
+                             void* q_out, int64_t q_out_stride, pivot_stream_t stream) {
+  clear_cuda_error();
+  pivot_status st = check_cache(cache);
+  if (st == PIVOT_OK) st = check_step(step, cache);
+  if (st != PIVOT_OK) return st;
+  if (dt != PIVOT_BF16 && dt != PIVOT_F32) return PIVOT_ERR_INVALID_ARG;
+  st = check_rows(k, k_stride, cache->kv_heads, cache->d, dt);
+  if (st == PIVOT_OK) st = check_rows(v, v_stride, cache->kv_heads, cache->d, dt);
+  if (st != PIVOT_OK) return st;
+  if (rot < 0 || rot > cache->d || rot % 16 || (interleaved != 0 && interleaved != 1)) return PIVOT_ERR_INVALID_ARG;
+  if (rot && (!cos || !sin || !aligned(cos, 16) || !aligned(sin, 16) ||
+              n_pos < (int64_t)step->table_width * cache->page_size))
+    return PIVOT_ERR_INVALID_ARG;
+  if (q) {
+    if (q_heads <= 0 || (q_out == q && q_out_stride != q_stride)) return PIVOT_ERR_INVALID_ARG;
+    st = check_rows(q, q_stride, q_heads, cache->d, dt);
+    if (st == PIVOT_OK) st = check_rows(q_out, q_out_stride, q_heads, cache->d, dt);
+    if (st != PIVOT_OK) return st;
+  }
+  if (step->rows == 0) return PIVOT_OK;
+  KvAppendArgs a{};
+  a.c = device_cache(*cache);
+  a.st = device_step(*step);
+  a.k = k;
+  a.v = v;
+  a.q = q;
+  a.q_out = q_out;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_stride = q_stride;
+  a.q_out_stride = q_out_stride;
+  a.cos = cos;
+  a.sin = sin;
+  a.n_pos = n_pos;
+  a.rot = rot;
+  a.interleaved = interleaved;
+  a.hq = q_heads;
+  a.is_bf16 = dt == PIVOT_BF16;
+  const cudaError_t e = launch_kv_append(a, sms(), reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv append kernel");
+}
+
+size_t pivot_kv_workspace_size(int64_t rows, int B, int q_heads, int kv_heads, int d, int topk, pivot_dtype dt) {
+  if (rows < 0 || rows >= 0x7FFFFFF0ll || B <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads > 1024 ||
+      q_heads % kv_heads || (d != 64 && d != 128) || topk < 0 || topk > 65536 || (dt != PIVOT_BF16 && dt != PIVOT_F32))
+    return 0;
+  return 256;
+}
+
+pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step* step, const void* q,
+                                int64_t q_stride, int q_heads, pivot_dtype dt, float scale, int64_t window,
+                                int64_t sinks, void* out, float* lse_opt, void* ws, size_t ws_bytes,
+                                pivot_stream_t stream) {
+  clear_cuda_error();
+  KvAttnArgs a{};
+  const pivot_status st = attention_args(cache, step, q, q_stride, q_heads, dt, scale, out, ws, &a);
+  if (st != PIVOT_OK) return st;
+  if (window < 0 || sinks < 0) return PIVOT_ERR_INVALID_ARG;
+  if (ws_bytes < pivot_kv_workspace_size(step->rows, step->B, q_heads, cache->kv_heads, cache->d, 0, dt))
+    return PIVOT_ERR_WORKSPACE_TOO_SMALL;
+  a.lse = lse_opt;
+  a.window = window;
+  a.sinks = sinks;
+  if (step->rows == 0) return PIVOT_OK;
+  const cudaError_t e = launch_kv_attn_simple(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv attention kernel");
+}
+
+pivot_status pivot_kv_attention_selected(const pivot_kv_cache* cache, const pivot_kv_step* step, const void* q,
+                                         int64_t q_stride, int q_heads, pivot_dtype dt, float scale,
+                                         const int32_t* indices, int64_t index_stride, int topk, void* out,
+                                         float* lse_opt, void* ws, size_t ws_bytes, pivot_stream_t stream) {
+  clear_cuda_error();
+  KvAttnArgs a{};
+  const pivot_status st = attention_args(cache, step, q, q_stride, q_heads, dt, scale, out, ws, &a);
+  if (st != PIVOT_OK) return st;
+  if (!indices || topk <= 0 || index_stride < topk) return PIVOT_ERR_INVALID_ARG;
+  if (topk > 65536) return PIVOT_ERR_UNSUPPORTED_SHAPE;
+  if (ws_bytes < pivot_kv_workspace_size(step->rows, step->B, q_heads, cache->kv_heads, cache->d, topk, dt))
+    return PIVOT_ERR_WORKSPACE_TOO_SMALL;
+  a.lse = lse_opt;
+  a.indices = indices;
+  a.idx_stride = index_stride;
+  a.topk = topk;
+  if (step->rows == 0) return PIVOT_OK;
+  const cudaError_t e = launch_kv_attn_simple(a, reinterpret_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv selected attention kernel");
+}
+
+}  // extern "C"
