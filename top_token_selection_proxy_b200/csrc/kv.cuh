@@ -4,6 +4,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <algorithm>
+
 #include "kernels.cuh"
 #include "ptx.cuh"
 
@@ -54,7 +56,8 @@ struct KvAttnArgs {
 };
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t s);
-cudaError_t launch_kv_attn_simple(const KvAttnArgs& a, cudaStream_t s);
+size_t kv_attn_workspace(int sms, int d);
+cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, cudaStream_t s);
 
 // The sequence b with off[b] <= r < off[b+1], or -1.
 __device__ __forceinline__ int kv_sequence_of(const KvStep& st, int64_t r) {
@@ -79,6 +82,18 @@ __device__ __forceinline__ int kv_page(const KvStep& st, const KvCache& c, int b
 __device__ __forceinline__ float kv_e4m3_to_f32(uint8_t x) {
   const __half_raw h = __nv_cvt_fp8_to_halfraw(x, __NV_E4M3);
   return __half2float(*reinterpret_cast<const __half*>(&h));
+}
+
+// Four consecutive output values.
+__device__ __forceinline__ void kv_store4(const KvAttnArgs& a, int64_t at, float x, float y, float z, float w,
+                                          bool bf16) {
+  if (bf16) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(x, y), hi = __floats2bfloat162_rn(z, w);
+    *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  } else {
+    *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(x, y, z, w);
+  }
 }
 
 // 2^e for an integer e in [-126, 127].

@@ -130,7 +130,7 @@ size_t pivot_kv_workspace_size(int64_t rows, int B, int q_heads, int kv_heads, i
   if (rows < 0 || rows >= 0x7FFFFFF0ll || B <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads > 1024 ||
       q_heads % kv_heads || (d != 64 && d != 128) || topk < 0 || topk > 65536 || (dt != PIVOT_BF16 && dt != PIVOT_F32))
     return 0;
-  return 256;
+  return kv_attn_workspace(sms(), d);
 }
 
 pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step* step, const void* q,
@@ -148,7 +148,7 @@ pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step
   a.window = window;
   a.sinks = sinks;
   if (step->rows == 0) return PIVOT_OK;
-  const cudaError_t e = launch_kv_attn_simple(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv_attn(a, sms(), ws, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv attention kernel");
 }
 
@@ -169,7 +169,7 @@ pivot_status pivot_kv_attention_selected(const pivot_kv_cache* cache, const pivo
   a.idx_stride = index_stride;
   a.topk = topk;
   if (step->rows == 0) return PIVOT_OK;
-  const cudaError_t e = launch_kv_attn_simple(a, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv_attn(a, sms(), ws, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv selected attention kernel");
 }
 

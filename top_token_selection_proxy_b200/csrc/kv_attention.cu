@@ -1,97 +1,800 @@
-// kv_attention.cu -- attention over the paged 8-bit cache: every visible position of a sequence, or each row's own
-// list of positions.
+// kv_attention.cu -- attention over the paged 8-bit cache with few query rows for a key head: every visible
+// position of a sequence, or each row's own list of positions.
 //
-// o = sum_s p_s v_s / sum_s p_s, p_s = exp2(scale2 * q . k_s - m), one pass with a running maximum m.
+// o = sum_s p_s v_s / sum_s p_s, p_s = 2^(z_s - m), z = scale2 * q . k (units of log 2), one pass over the keys.
+// A key is payload * 2^e with one e for 16 tokens and head, so z = (q . payload) * 2^e scale2, and the output sum
+// takes weights p * 2^e.  Two running maxima keep both sums in range whatever the scales are: m of z for the
+// denominator, m' of z + e for the numerator.  Weights enter the product as fp16 values of 2^14 2^(z + e - m').
+//
+// What bounds it: the cache's bytes (2 d and a little for each token and key head, read once for up to 16 query
+// rows).  So the payload goes to registers in the order in which the matrix instruction wants it, without a
+// detour: in a product the order of the summed index is free, hence a lane that holds 16 consecutive dims of a key
+// holds the operands of 4 steps of m16n8k16, and a lane that holds 16 consecutive dims of a value those of 16
+// column tiles.  Each lane copies exactly the 16-byte pieces that it will use itself into its own places of shared
+// memory (cp.async), so the ring needs no barrier: every warp runs through its own tokens alone.
+//
+// Work is cut evenly whatever the lengths are: all tiles of 128 tokens of all (sequence, key head, 16 query rows)
+// stand in one line, and every CTA takes an equal stretch of it.  A stretch that begins or ends inside an item
+// leaves a partial result, which kv_merge_kernel joins in a fixed order.
+#include <cuda_fp16.h>
+
 #include "kv.cuh"
 
 namespace pivot {
 namespace {
 
-constexpr int kSimple = 128;
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kRowsT = 16;              // query rows of an item
+constexpr int kWTok = 32;               // tokens a warp takes at a time (two blocks)
+constexpr int kTile = kWTok * kWarps;   // tokens of a tile
+constexpr float kLift = 14.f;           // weights stand 2^14 above the largest term: fp16 keeps 11 bits down to 2^-28
 
-// One CTA for a row and query head: 128 positions at a time, a thread scores one and then sums one output dim.
-template <bool BF16, bool SEL>
-__global__ void __launch_bounds__(kSimple) kv_attn_simple_kernel(const KvAttnArgs a) {
-  __shared__ float qs[128], w[kSimple];
-  __shared__ int64_t at[kSimple];
-  __shared__ float red[kSimple / 32];
-  const int64_t r = blockIdx.x;
-  const int j = blockIdx.y, tid = threadIdx.x, d = a.c.d, head = j / a.group;
-  const int b = kv_sequence_of(a.st, r);
-  if (b < 0) return;
-  const int64_t pos = a.st.lens[b] - a.st.off[b + 1] + r;
+// What a CTA leaves for the merge when it began an item that others end.
+struct alignas(16) KvOpen {
+  int64_t item_end, total;  // in tiles of the line
+  int64_t row0;             // first query row's index
+  int32_t stretch, cta_count, head0, rr0, valid, open;
+};
+
+__host__ __device__ constexpr size_t part_floats(int d) { return (size_t)kRowsT * (d + 4); }  // o, then m', m, l, 0
+
+struct KvLine {
+  KvOpen* open;   // [ctas]
+  float* part;    // [ctas][2][part_floats]
+  int* status;
+};
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ __forceinline__ float quad_max(float x) {
+  x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+  return fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+}
+__device__ __forceinline__ float quad_sum(float x) {
+  x += __shfl_xor_sync(~0u, x, 1);
+  return x + __shfl_xor_sync(~0u, x, 2);
+}
+
+// 16 (or 8) bytes to shared memory; nothing is read and zeros are written where `live` is false.
+template <int N>
+__device__ __forceinline__ void cp_async_or_zero(uint32_t dst, const void* src, bool live) {
+  if (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(live ? 8 : 0) : "memory");
+}
+
+// ---------------------------------------------------------------- the line of tiles
+struct Extent {      // of one sequence
+  int64_t first;     // position of its first row
+  int hi;            // last position there is (-1: none)
+  int sink_tiles, lo_tile, tiles, row_tiles;
+};
+
+__device__ __forceinline__ Extent extent_of(const KvAttnArgs& a, int b) {
+  Extent e;
+  const int64_t n = a.st.off[b + 1] - a.st.off[b], len = a.st.lens[b];
   const int64_t cap = (int64_t)a.st.width * a.c.ps;
-  const int64_t n = SEL ? (pos < 0 ? 0 : a.topk) : min64(pos + 1, cap);
-  if (tid < d) {
-    const int64_t qi = r * a.q_stride + (int64_t)j * d + tid;
-    qs[tid] = BF16 ? __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(a.q)[qi])
-                   : reinterpret_cast<const float*>(a.q)[qi];
-  }
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (int64_t i0 = 0; i0 < n; i0 += kSimple) {
-    __syncthreads();
-    const int64_t i = i0 + tid;
-    int64_t s = -1;
-    if (i < n) s = SEL ? (int64_t)a.indices[r * a.idx_stride + i] : i;
-    bool seen = s >= 0 && s <= pos && s < cap;
-    if (!SEL && a.window > 0) seen = seen && (s > pos - a.window || s < a.sinks);
-    int64_t slot = -1;
-    float x = -INFINITY;
-    if (seen) {
-      const int pg = kv_page(a.st, a.c, b, (uint32_t)s);
-      if (pg >= 0) {
-        const int in = (int)(s % a.c.ps);
-        const int64_t ph = (int64_t)pg * a.c.hk + head;
-        slot = ph * a.c.ps + in;
-        const uint8_t* k = a.c.k + slot * d;
-        float dot = 0.f;
-        for (int e = 0; e < d; ++e) dot = fmaf(qs[e], kv_e4m3_to_f32(k[e]), dot);
-        x = dot * kv_scale(a.c.ke[ph * (a.c.ps / kKvBlock) + in / kKvBlock]) * a.scale2;
-      }
-    }
-    float t = x;
+  e.first = len - n;
+  e.hi = (int)max64(min64(len, cap) - 1, -1);
+  int64_t lo = 0;
+  if (a.window > 0) lo = min64(max64(e.first - a.window + 1, 0), max64(e.hi, 0));
+  e.lo_tile = (int)(lo / kTile);
+  e.sink_tiles = a.window > 0 ? (int)min64((min64(a.sinks, e.hi + 1) + kTile - 1) / kTile, e.lo_tile) : 0;
+  e.tiles = e.sink_tiles + max(e.hi, 0) / kTile - e.lo_tile + 1;
+  e.row_tiles = n > 0 ? (int)((n * a.group + kRowsT - 1) / kRowsT) : 0;
+  return e;
+}
+
+__device__ __forceinline__ int64_t weight_of(const KvAttnArgs& a, int b) {
+  if (b >= a.st.B) return 0;
+  const Extent e = extent_of(a, b);
+  return (int64_t)a.c.hk * e.row_tiles * e.tiles;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int D, bool BF16, bool SEL>
+struct Shape {
+  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kKPieces = 4 * (D / 64);         // 16-byte pieces of keys a lane holds of 32 tokens
+  static constexpr int kVBytes = D / 8;                 // bytes of a value a lane holds
+  static constexpr int kStageBytes = 32 * (kKPieces * 16 + 8 * kVBytes);  // a warp's
+  static constexpr int kRing = kWarps * kStages * kStageBytes;
+  static constexpr int kQParts = BF16 ? 1 : 3;
+  static constexpr int kQBytes = BF16 ? 0 : kQParts * (D / 16) * 32 * 16;
+  static constexpr size_t kBytes = kRing + kQBytes + 64 * sizeof(float) * kWarps;
+};
+
+template <int D, bool BF16, bool SEL>
+__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const KvAttnArgs a, const KvLine line) {
+  using S = Shape<D, BF16, SEL>;
+  constexpr int NK = D / 16, NT = D / 8, kStages = S::kStages;
+  extern __shared__ __align__(16) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, tig = lane % 4;
+  float* const stats = reinterpret_cast<float*>(smem + S::kRing + S::kQBytes);  // [warp][16 rows][m', m, l]
+  const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
+  if (blockIdx.x == 0 && tid == 0) *line.status = 0;
+
+  // this CTA's stretch of the line
+  int64_t total = 0, sel_rows = 0;
+  const int sel_rt = (a.group + kRowsT - 1) / kRowsT, sel_tiles = (a.topk + kTile - 1) / kTile;
+  if (SEL) {
+    sel_rows = max64(min64(a.st.off[a.st.B], a.st.rows), 0);
+    total = sel_rows * a.c.hk * sel_rt * sel_tiles;
+  } else {
+    for (int b = lane; b < a.st.B; b += 32) total += weight_of(a, b);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) t = fmaxf(t, __shfl_xor_sync(~0u, t, o));
-    if (tid % 32 == 0) red[tid / 32] = t;
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+  }
+  const int64_t ctas = min64(gridDim.x, total);
+  KvOpen* const open = line.open + blockIdx.x;
+  if (tid == 0) open->open = 0;
+  if (blockIdx.x >= ctas) return;
+  int64_t at = total * blockIdx.x / ctas;
+  const int64_t stop = total * (blockIdx.x + 1) / ctas;
+
+  // the item that holds tile `at`: sequence b, item x of it, tile t of the item
+  int b = 0, x = 0, t = 0, per_b = 0;
+  int64_t row = 0;
+  Extent e{};
+  if (SEL) {
+    const int64_t item = at / sel_tiles;
+    t = (int)(at - item * sel_tiles);
+    per_b = a.c.hk * sel_rt;
+    row = item / per_b;
+    x = (int)(item - row * per_b);
+    e.tiles = sel_tiles;
+    e.row_tiles = sel_rt;
+    b = kv_sequence_of(a.st, row);
+  } else {
+    int64_t run = 0;
+    for (int b0 = 0;; b0 += 32) {
+      if (b0 >= a.st.B) return;  // only where the lengths changed under the call
+      const int64_t w = weight_of(a, b0 + lane);
+      int64_t inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += up;
+      }
+      const unsigned hit = __ballot_sync(~0u, run + inc > at);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        b = b0 + l;
+        at -= run + __shfl_sync(~0u, inc - w, l);  // tiles into the sequence, for a moment
+        break;
+      }
+      run += __shfl_sync(~0u, inc, 31);
+    }
+    e = extent_of(a, b);
+    per_b = a.c.hk * e.row_tiles;
+    x = (int)(at / e.tiles);
+    t = (int)(at - (int64_t)x * e.tiles);
+    at = total * blockIdx.x / ctas;
+  }
+
+  while (at < stop) {
+    const int t0 = t, t1 = (int)min64(e.tiles, t + (stop - at));
+    const int h = x / e.row_tiles, rr0 = (x - h * e.row_tiles) * kRowsT;  // key head, first of its query rows
+    int64_t row0, first;
+    int n, hi;
+    if (SEL) {
+      row0 = row;
+      n = 1;
+      first = b < 0 ? -1 : a.st.lens[b] - a.st.off[b + 1] + row;
+      hi = (int)max64(min64(first, (int64_t)a.st.width * a.c.ps - 1), -1);
+    } else {
+      row0 = a.st.off[b];
+      n = (int)(a.st.off[b + 1] - row0);
+      first = e.first;
+      hi = e.hi;
+    }
+    const int valid = (int)min64(kRowsT, (int64_t)n * a.group - rr0);
+    // positions of this lane's two rows, and of the item's first and last; far below zero they see nothing
+    const int64_t p_lo = first + rr0 / a.group, p_hi = first + (rr0 + valid - 1) / a.group;
+    const int64_t pr[2] = {first + (rr0 + min(g, valid - 1)) / a.group, first + (rr0 + min(g + 8, valid - 1)) / a.group};
+
+    // q: this lane's operands, scaled by a power of two so that the row's largest lies in [2^14, 2^15)
+    uint32_t qa[BF16 ? NK : 1][4];
+    float unit[2];  // scale2 / that power
+    {
+      float v[2][2 * NK * 2];
+      uint4* const qs = reinterpret_cast<uint4*>(smem + S::kRing);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int rr = rr0 + g + 8 * i, in = g + 8 * i;
+        const int64_t r = row0 + rr / a.group;
+        const bool live = in < valid && r < a.st.rows;
+        const int64_t base = r * a.q_stride + (int64_t)(h * a.group + rr % a.group) * D + 16 * tig;
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int j = 0; j < 16; j += 4) {
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            if (live) {
+              if (BF16) {
+                const uint2 w = *reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.q) + base + 64 * c + j);
+                f[0] = __uint_as_float(w.x << 16), f[1] = __uint_as_float(w.x & 0xFFFF0000u);
+                f[2] = __uint_as_float(w.y << 16), f[3] = __uint_as_float(w.y & 0xFFFF0000u);
+              } else {
+                const float4 w = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + base + 64 * c + j);
+                f[0] = w.x, f[1] = w.y, f[2] = w.z, f[3] = w.w;
+              }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              v[i][16 * c + j + k] = f[k];
+              top = fmaxf(top, fabsf(f[k]));
+            }
+          }
+        top = quad_max(top);
+        const int ex = top > 0.f && top <= 3.402823466e38f ? max((int)(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
+        unit[i] = a.scale2 * kv_exp2i(ex);
+        const float down = kv_exp2i(-ex);
+#pragma unroll
+        for (int k = 0; k < D / 4; ++k) v[i][k] *= down;
+      }
+#pragma unroll
+      for (int ks = 0; ks < NK; ++ks) {
+        if (BF16) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)  // a0: row g, a1: row g + 8, a2, a3: the same rows' next two dims
+            qa[ks][k] = pack_f16(v[k & 1][4 * ks + (k & 2)], v[k & 1][4 * ks + (k & 2) + 1]);
+        } else if (warp == 0) {  // fp32: three fp16 parts hold all 24 bits; kept in shared memory
+#pragma unroll
+          for (int part = 0; part < S::kQParts; ++part) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              float* f = &v[k & 1][4 * ks + (k & 2)];
+              w[k] = pack_f16(f[0], f[1]);
+              const __half2 hh = *reinterpret_cast<const __half2*>(&w[k]);
+              f[0] -= __low2float(hh);
+              f[1] -= __high2float(hh);
+            }
+            qs[(part * NK + ks) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (!BF16) __syncthreads();
+    }
+
+    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, mp[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+
+    // The tiles in which some row of the item can see something: of [t0, t1) those of the first tokens, then those
+    // from w0 on.
+    int tb = t1, w0 = t0, ahead = 0;
+    if (!SEL) {
+      const int last = (int)(min64(p_hi, hi) < 0 ? -1 : min64(p_hi, hi) / kTile);  // tile of the last position
+      tb = min(tb, last < e.lo_tile ? min(e.sink_tiles, last + 1) : e.sink_tiles + last - e.lo_tile + 1);
+      if (a.window > 0) {
+        const int sinks_end = (int)((min64(a.sinks, hi + 1) + kTile - 1) / kTile);
+        const int from = (int)(min64(max64(p_lo - a.window + 1, 0), max(hi, 0)) / kTile);
+        ahead = max(min(tb, sinks_end) - t0, 0);
+        w0 = max(max(t0, sinks_end), e.sink_tiles + from - e.lo_tile);
+      }
+    } else if (hi < 0) {
+      tb = t0;
+    }
+    const int steps = ahead + max(tb - w0, 0);
+    auto base_of = [&](int step) {  // first of this warp's tokens (positions, or places in the list)
+      const int tt = step < ahead ? t0 + step : w0 + step - ahead;
+      const int tile = SEL || tt < e.sink_tiles ? tt : e.lo_tile + tt - e.sink_tiles;
+      return tile * kTile + warp * kWTok;
+    };
+
+    // Look-ups run ahead of the copies: list entries (selected), then pages, then the copies and the exponents.
+    const int32_t* const list = SEL ? a.indices + row0 * a.idx_stride : nullptr;
+    auto load_entry = [&](int step) -> int {  // a lane's position of a step; -1: none
+      if (step >= steps) return -1;
+      const int i = base_of(step) + lane;
+      if (!SEL) return i;
+      const int s = i < a.topk ? __ldg(list + i) : -1;
+      return s <= hi ? s : -1;
+    };
+    auto load_page = [&](int s) -> int {  // page of a lane's position; -1: absent
+      if (s < 0 || s > hi) return -1;
+      return kv_page(a.st, a.c, b, (uint32_t)s);
+    };
+    // the copies of one step; returns the lane's token's packed (ke, ve) with bit 16 set where it is present
+    auto issue = [&](int step, int s, int page) -> uint32_t {
+      uint32_t ex = 0;
+      if (step < steps) {
+        const uint32_t dst = ring + (step % kStages) * S::kStageBytes + lane * 16;
+        const uint32_t in = page >= 0 ? (uint32_t)s % (uint32_t)a.c.ps : 0u;
+        const int slot = page >= 0 ? (page * a.c.hk + h) * a.c.ps + (int)in : -1;  // row of the cache
+        if (page >= 0) {
+          const int64_t be = ((int64_t)page * a.c.hk + h) * (a.c.ps / kKvBlock) + in / kKvBlock;
+          ex = (uint8_t)__ldg(a.c.ke + be) | ((uint32_t)(uint8_t)__ldg(a.c.ve + be) << 8) | 0x10000u;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int sl = __shfl_sync(~0u, slot, 8 * j + g);
+          const uint8_t* src = a.c.k + (int64_t)max(sl, 0) * D + 16 * tig;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            cp_async_or_zero<16>(dst + (j * (D / 64) + c) * 512, src + 64 * c, sl >= 0);
+        }
+        const uint32_t vdst = ring + (step % kStages) * S::kStageBytes + S::kKPieces * 512 + lane * S::kVBytes;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int sl = __shfl_sync(~0u, slot, 16 * (j / 4) + 8 * (j / 2 % 2) + 2 * tig + j % 2);
+          cp_async_or_zero<S::kVBytes>(vdst + j * 32 * S::kVBytes, a.c.v + (int64_t)max(sl, 0) * D + S::kVBytes * g,
+                                       sl >= 0);
+        }
+      }
+      cp_async_commit();
+      return ex;
+    };
+
+    uint32_t exps[kStages];  // of the steps in flight, the next one first
+    int s_next, page_next, s_after;
+    {
+      int s[kStages + 1], pg[kStages + 1];
+#pragma unroll
+      for (int i = 0; i <= kStages; ++i) s[i] = load_entry(i);
+#pragma unroll
+      for (int i = 0; i <= kStages; ++i) pg[i] = load_page(s[i]);
+#pragma unroll
+      for (int i = 0; i < kStages; ++i) exps[i] = issue(i, s[i], pg[i]);
+      s_next = s[kStages];
+      page_next = pg[kStages];
+      s_after = load_entry(kStages + 1);
+    }
+
+    for (int step = 0; step < steps; ++step) {
+      const uint32_t ex = exps[0];
+      cp_async_wait<kStages - 1>();  // a lane reads only what it copied itself
+      const uint8_t* const kst = smem + (ring - smem_u32(smem)) + (step % kStages) * S::kStageBytes;
+      const uint8_t* const vst = kst + S::kKPieces * 512;
+      const int base = base_of(step);
+
+      // scores: 4 tiles of 8 tokens
+      float z[4][4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) z[j][0] = z[j][1] = z[j][2] = z[j][3] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        uint4 kw[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          kw[j] = *reinterpret_cast<const uint4*>(kst + (j * (D / 64) + c) * 512 + lane * 16);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          uint32_t b0[4], b1[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint32_t w = k == 0 ? kw[j].x : k == 1 ? kw[j].y : k == 2 ? kw[j].z : kw[j].w;
+            b0[j] = cvt_e4m3x2(w);
+            b1[j] = cvt_e4m3x2(w >> 16);
+          }
+          if (BF16) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) mma16816(z[j], qa[BF16 ? 4 * c + k : 0], b0[j], b1[j]);
+          } else {
+#pragma unroll
+            for (int part = S::kQParts - 1; part >= 0; --part) {
+              const uint4 w = reinterpret_cast<const uint4*>(smem + S::kRing)[(part * NK + 4 * c + k) * 32 + lane];
+              const uint32_t aq[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) mma16816(z[j], aq, b0[j], b1[j]);
+            }
+          }
+        }
+      }
+
+      // scale, mask
+      float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
+      uint32_t te[4][2];  // (ke, ve, present) of the two tokens that this lane holds in each tile
+      bool part_seen = false;  // some row sees a token of this step that another does not
+      const bool whole = !SEL && __all_sync(~0u, ex >> 16) && base + kWTok - 1 <= min64(p_lo, hi) &&
+                         (a.window <= 0 || base > p_hi - a.window || base + kWTok <= a.sinks);
+      if (SEL) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) te[j][k] = __shfl_sync(~0u, ex, 8 * j + 2 * tig + k);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; j += 2) {  // a block's tokens share one
+          const uint32_t w = __shfl_sync(~0u, ex, 8 * j);
+          te[j][0] = te[j][1] = te[j + 1][0] = te[j + 1][1] = w;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float ks = kv_scale((int8_t)te[j][k]);
+          const float ve = (float)(int8_t)(te[j][k] >> 8);
+          const int s = base + 8 * j + 2 * tig + k;
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            float v = z[j][2 * i + k] * (unit[i] * ks);
+            if (SEL) {
+              if (!(te[j][k] >> 16)) v = -INFINITY;
+            } else if (!whole) {
+              const bool seen = (te[j][k] >> 16) && s <= hi && s <= pr[i] &&
+                                (a.window <= 0 || s > pr[i] - a.window || s < a.sinks);
+              if (!seen) v = -INFINITY;
+            }
+            z[j][2 * i + k] = v;
+            top[i] = fmaxf(top[i], v);
+            topv[i] = fmaxf(topv[i], v + ve);
+          }
+        }
+      if (!SEL && !whole) part_seen = true;
+
+      // the running maxima
+      float lift[2];
+      bool moved = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float mn = fmaxf(m[i], quad_max(top[i])), mpn = fmaxf(mp[i], quad_max(topv[i]));
+        moved |= mpn != mp[i];
+        top[i] = mpn;
+        if (mn != m[i]) l[i] *= ex2(m[i] - mn);
+        m[i] = mn;
+        lift[i] = mn == -INFINITY ? 0.f : mn;
+      }
+      if (__any_sync(~0u, moved)) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f = top[i] == mp[i] ? 1.f : ex2(mp[i] - top[i]);
+          mp[i] = top[i];
+#pragma unroll
+          for (int n8 = 0; n8 < NT; ++n8) o[n8][2 * i] *= f, o[n8][2 * i + 1] *= f;
+        }
+      }
+      // weights: p for the sum, p * 2^(ve + m - m' + 14) for the product
+      uint32_t pa[2][4], pb[2][4];  // operands of the two blocks; the rest of them (fp32)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float off = lift[i] - (mp[i] == -INFINITY ? 0.f : mp[i]) + kLift;
+          float w[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float p = ex2(z[j][2 * i + k] - lift[i]);
+            l[i] += p;
+            w[k] = p * ex2(fminf((float)(int8_t)(te[j][k] >> 8) + off, 126.f));  // finite: p may be a masked zero
+          }
+          const uint32_t hw = pack_f16(w[0], w[1]);
+          pa[j / 2][2 * (j % 2) + i] = hw;
+          if (!BF16) {
+            const __half2 hh = *reinterpret_cast<const __half2*>(&hw);
+            pb[j / 2][2 * (j % 2) + i] = pack_f16(w[0] - __low2float(hh), w[1] - __high2float(hh));
+          }
+        }
+
+      // output sums: 16 tokens a block, NT tiles of 8 dims
+      constexpr int VW = S::kVBytes / 4;  // words a lane holds of a value
+      auto value = [&](int u, uint32_t (&w)[4][VW]) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint8_t* at4 = vst + (4 * u + j) * 32 * S::kVBytes + lane * S::kVBytes;
+          if (VW == 4) {
+            const uint4 r = *reinterpret_cast<const uint4*>(at4);
+            w[j][0] = r.x, w[j][1] = r.y, w[j][VW == 4 ? 2 : 0] = r.z, w[j][VW == 4 ? 3 : 1] = r.w;
+          } else {
+            const uint2 r = *reinterpret_cast<const uint2*>(at4);
+            w[j][0] = r.x, w[j][1] = r.y;
+          }
+        }
+      };
+      // A weight of zero does not hide a NaN value from a matrix instruction.  Tokens that no row sees were zeroed
+      // on the way in; one that some rows see and others do not gets its product row by row.
+      bool odd = false;
+      if (part_seen) {
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t w[4][VW];
+          value(u, w);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < VW; ++k) odd |= __vcmpeq4(w[j][k] & 0x7F7F7F7Fu, 0x7F7F7F7Fu) != 0;
+        }
+        odd = __any_sync(~0u, odd);
+      }
+#pragma unroll 1
+      for (int only = odd ? 0 : -1; only < (odd ? valid : 0); ++only) {
+        const int64_t p = first + (rr0 + max(only, 0)) / a.group;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          uint32_t w[4][VW];
+          value(u, w);
+          if (odd) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int s = base + 16 * u + 8 * (j / 2) + 2 * tig + j % 2;
+              if (!(s <= p && (a.window <= 0 || s > p - a.window || s < a.sinks))) {
+#pragma unroll
+                for (int k = 0; k < VW; ++k) w[j][k] = 0u;
+              }
+            }
+          }
+#pragma unroll
+          for (int k = 0; k < VW; ++k) {
+            const uint32_t l0 = __byte_perm(w[0][k], w[1][k], 0x5140), h0 = __byte_perm(w[0][k], w[1][k], 0x7362);
+            const uint32_t l1 = __byte_perm(w[2][k], w[3][k], 0x5140), h1 = __byte_perm(w[2][k], w[3][k], 0x7362);
+            const uint32_t b0[4] = {cvt_e4m3x2(l0), cvt_e4m3x2(l0 >> 16), cvt_e4m3x2(h0), cvt_e4m3x2(h0 >> 16)};
+            const uint32_t b1[4] = {cvt_e4m3x2(l1), cvt_e4m3x2(l1 >> 16), cvt_e4m3x2(h1), cvt_e4m3x2(h1 >> 16)};
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4) {
+              if (BF16 && !odd) {
+                mma16816(o[4 * k + q4], pa[u], b0[q4], b1[q4]);
+              } else {  // fp32: a block's own sum first, then one addition; odd: of one row alone
+                float t4[4] = {0.f, 0.f, 0.f, 0.f};
+                if (!BF16) mma16816(t4, pb[u], b0[q4], b1[q4]);
+                mma16816(t4, pa[u], b0[q4], b1[q4]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  if (!odd || only == g + 8 * (i / 2)) o[4 * k + q4][i] += t4[i];
+              }
+            }
+          }
+        }
+      }
+
+      // the next copies go where this step's were; every lane is past its own reads
+#pragma unroll
+      for (int i = 0; i + 1 < kStages; ++i) exps[i] = exps[i + 1];
+      exps[kStages - 1] = issue(step + kStages, s_next, page_next);
+      page_next = load_page(s_after);
+      s_next = s_after;
+      s_after = load_entry(step + kStages + 2);
+    }
+
+    // the warps' results together, in shared memory
+    cp_async_wait<0>();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) l[i] = quad_sum(l[i]);
+    if (tig == 0) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        float* st = stats + warp * 64 + (g + 8 * i) * 4;
+        st[0] = mp[i], st[1] = m[i], st[2] = l[i];
+      }
+    }
+    __syncthreads();  // also: every warp is done with its ring
+    float* const sums = reinterpret_cast<float*>(smem);  // [warp][16][D]
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = g + 8 * i;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w * 64 + r * 4]);
+      const float f = mp[i] == -INFINITY ? 0.f : ex2(mp[i] - top);
+      // a row that saw nothing here has sums of zero, whatever its queries are
+      float* to = sums + (warp * kRowsT + r) * D + 2 * NT * tig;
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+#pragma unroll
+        for (int n8 = 0; n8 < NT; n8 += 4)
+          *reinterpret_cast<float4*>(to + k * NT + n8) =
+              make_float4(mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8][2 * i + k] * f,
+                          mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8 + 1][2 * i + k] * f,
+                          mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8 + 2][2 * i + k] * f,
+                          mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8 + 3][2 * i + k] * f);
+    }
     __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    const float f = mn == -INFINITY ? 1.f : exp2f(m - mn);
-    w[tid] = slot < 0 ? 0.f : exp2f(x - mn);
-    at[tid] = slot;
-    __syncthreads();
-    l *= f;
-    acc *= f;
-    m = mn;
-    for (int e = 0; e < kSimple; ++e) {
-      if (at[e] < 0) continue;
-      l += w[e];
-      if (tid < d) {
-        const int64_t ph = at[e] / a.c.ps, in = at[e] % a.c.ps;
-        acc = fmaf(w[e], kv_e4m3_to_f32(a.c.v[at[e] * d + tid]) *
-                             kv_scale(a.c.ve[ph * (a.c.ps / kKvBlock) + in / kKvBlock]), acc);
+    const bool all = t0 == 0 && t1 == e.tiles;
+    float* const part = line.part + ((int64_t)blockIdx.x * 2 + (t0 == 0)) * part_floats(D);
+    constexpr int kLanes = D / 4;  // threads of a row
+    for (int r = tid / kLanes; r < valid; r += kThreads / kLanes) {
+      const int c = tid % kLanes * 4;
+      float mt = -INFINITY, mpt = -INFINITY, lt = 0.f;
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        mpt = fmaxf(mpt, stats[w * 64 + r * 4]);
+        mt = fmaxf(mt, stats[w * 64 + r * 4 + 1]);
+        const float4 v = *reinterpret_cast<const float4*>(sums + (w * kRowsT + r) * D + c);
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float ml = stats[w * 64 + r * 4 + 1], lw = stats[w * 64 + r * 4 + 2];
+        lt += ml == -INFINITY ? lw : lw * ex2(ml - mt);  // -inf: zero, or NaN of a score
+      }
+      if (all) {
+        const int64_t rr = row0 + (rr0 + r) / a.group;
+        if (rr < a.st.rows) {
+          const int j = h * a.group + (rr0 + r) % a.group;
+          const float f = lt == 0.f ? 0.f : ex2(mpt - mt - kLift) / lt;
+          kv_store4(a, (rr * a.hq + j) * (int64_t)D + c, s.x * f, s.y * f, s.z * f, s.w * f, BF16);
+          if (a.lse && c == 0) a.lse[rr * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (mt + log2f(lt));
+        }
+      } else {
+        *reinterpret_cast<float4*>(part + r * D + c) = s;
+        if (c == 0) *reinterpret_cast<float4*>(part + kRowsT * D + r * 4) = make_float4(mpt, mt, lt, 0.f);
+      }
+    }
+    if (!all && t0 == 0 && tid == 0)
+      *open = {at - t0 + e.tiles, total, row0, (int)blockIdx.x, (int)ctas, h * a.group, rr0, valid, 1};
+    __syncthreads();  // the ring is free again
+
+    at += t1 - t0;
+    t = 0;
+    if (++x == per_b && at < stop) {
+      x = 0;
+      if (SEL) {
+        ++row;
+        if (row >= a.st.off[b + 1]) b = kv_sequence_of(a.st, row);
+      } else {
+        do e = extent_of(a, ++b);
+        while (e.row_tiles == 0 && b + 1 < a.st.B);
+        if (e.row_tiles == 0) break;  // as above
+        per_b = a.c.hk * e.row_tiles;
       }
     }
   }
-  if (tid < d) {
-    const float o = l == 0.f ? 0.f : acc / l;
-    const int64_t oi = (r * a.hq + j) * (int64_t)d + tid;
-    if (BF16) reinterpret_cast<__nv_bfloat16*>(a.out)[oi] = __float2bfloat16_rn(o);
-    else reinterpret_cast<float*>(a.out)[oi] = o;
+}
+
+// Joins the partial results of an item that several CTAs worked on: block (c, y) those that CTA c began.  Warps take
+// every eighth of them, lanes four dims; the order of the sums is fixed by the line alone.
+constexpr int kMergeWarps = 8;
+template <int D, bool BF16>
+__global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvAttnArgs a, const KvLine line) {
+  __shared__ float sums[kMergeWarps][D + 4];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const KvOpen op = line.open[blockIdx.x];
+  if (!op.open) return;
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  // CTAs c + 1 .. c + more work on the item's other tiles
+  int more = 0;
+  {
+    int64_t lo = op.stretch, hi = op.cta_count;  // begin(lo) < item_end <= begin(hi)
+    while (hi - lo > 1) {
+      const int64_t mid = (lo + hi) >> 1;
+      if (op.total * mid / op.cta_count < op.item_end) lo = mid;
+      else hi = mid;
+    }
+    more = (int)(lo - op.stretch);
   }
-  if (a.lse && tid == 0) a.lse[r * a.hq + j] = l == 0.f ? -INFINITY : 0.6931471805599453f * m + logf(l);
+  auto part_of = [&](int i) {  // the first one stands in the place of an item begun, the others in that of one ended
+    return line.part + ((int64_t)(op.stretch + i) * 2 + (i == 0)) * part_floats(D);
+  };
+  for (int r = blockIdx.y; r < op.valid; r += gridDim.y) {
+    float mp = -INFINITY, m = -INFINITY;
+    for (int i = lane; i <= more; i += 32) {
+      const float4 s = *reinterpret_cast<const float4*>(part_of(i) + kRowsT * D + r * 4);
+      mp = fmaxf(mp, s.x);
+      m = fmaxf(m, s.y);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+      mp = fmaxf(mp, __shfl_xor_sync(~0u, mp, o));
+      m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    }
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const bool mine = lane * 4 < D;
+#pragma unroll 4
+    for (int i = warp; i <= more; i += kMergeWarps) {
+      const float* p = part_of(i);
+      const float4 s = *reinterpret_cast<const float4*>(p + kRowsT * D + r * 4);
+      l += s.y == -INFINITY ? s.z : s.z * ex2(s.y - m);
+      const float f = s.x == -INFINITY ? (s.z == 0.f ? 0.f : 1.f) : ex2(s.x - mp);
+      if (mine) {
+        const float4 v = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
+        acc.x += f == 0.f ? 0.f : v.x * f, acc.y += f == 0.f ? 0.f : v.y * f;
+        acc.z += f == 0.f ? 0.f : v.z * f, acc.w += f == 0.f ? 0.f : v.w * f;
+      }
+    }
+    if (mine) *reinterpret_cast<float4*>(&sums[warp][lane * 4]) = acc;
+    if (lane == 0) sums[warp][D] = l;
+    __syncthreads();
+    if (warp == 0) {
+      float lt = 0.f;
+      acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kMergeWarps; ++w) {
+        lt += sums[w][D];
+        if (mine) acc.x += sums[w][lane * 4], acc.y += sums[w][lane * 4 + 1], acc.z += sums[w][lane * 4 + 2],
+                  acc.w += sums[w][lane * 4 + 3];
+      }
+      const int64_t row = op.row0 + (op.rr0 + r) / a.group;
+      if (row < a.st.rows) {
+        const int j = op.head0 + (op.rr0 + r) % a.group;
+        const float f = lt == 0.f ? 0.f : ex2(mp - m - kLift) / lt;
+        if (mine) kv_store4(a, (row * a.hq + j) * (int64_t)D + lane * 4, acc.x * f, acc.y * f, acc.z * f, acc.w * f, BF16);
+        if (a.lse && lane == 0) a.lse[row * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(lt));
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// CTAs of the line: as many as the device holds at once, but no more than there can be tiles.
+int line_ctas(int sms, const KvAttnArgs& a) {
+  const int64_t per = a.is_bf16 ? 3 : 2;
+  int64_t tiles;
+  if (a.indices) {
+    tiles = a.st.rows * a.c.hk * ((a.group + kRowsT - 1) / kRowsT) * ((a.topk + kTile - 1) / kTile);
+  } else {
+    const int64_t items = a.st.B + a.st.rows * a.group / kRowsT;
+    const int64_t cap = (int64_t)a.st.width * a.c.ps;
+    tiles = items * a.c.hk * ((cap + kTile - 1) / kTile + 1);
+  }
+  return (int)std::max<int64_t>(1, std::min<int64_t>(per * sms, tiles));
+}
+
+KvLine carve_line(void* ws, int ctas) {
+  char* p = static_cast<char*>(ws);
+  KvLine line;
+  line.status = reinterpret_cast<int*>(p);
+  line.open = reinterpret_cast<KvOpen*>(p + 256);
+  line.part = reinterpret_cast<float*>(p + 256 + (size_t)ctas * sizeof(KvOpen));
+  return line;
+}
+
+template <int D, bool BF16, bool SEL>
+cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaStream_t s) {
+  using Sh = Shape<D, BF16, SEL>;
+  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D, BF16, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                       (int)Sh::kBytes);
+  if (e != cudaSuccess) return e;
+  kv_attn_kernel<D, BF16, SEL><<<ctas, kThreads, Sh::kBytes, s>>>(a, line);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || ctas == 1) return e;
+  // Few items cut into many parts: one block for each row of an item, so that a long join has 16 of them.
+  const int64_t items = a.indices ? a.st.rows * a.c.hk : (a.st.B + a.st.rows * a.group / kRowsT) * (int64_t)a.c.hk;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)ctas, ctas > 4 * items ? kRowsT : 2);
+  cfg.blockDim = dim3(32 * kMergeWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // its launch overlaps the kernel before it
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, BF16>, a, line);
 }
 
 }  // namespace
 
-cudaError_t launch_kv_attn_simple(const KvAttnArgs& a, cudaStream_t s) {
-  const dim3 grid((unsigned)a.st.rows, (unsigned)a.hq);
-  if (a.indices)
-    a.is_bf16 ? kv_attn_simple_kernel<true, true><<<grid, kSimple, 0, s>>>(a)
-              : kv_attn_simple_kernel<false, true><<<grid, kSimple, 0, s>>>(a);
-  else
-    a.is_bf16 ? kv_attn_simple_kernel<true, false><<<grid, kSimple, 0, s>>>(a)
-              : kv_attn_simple_kernel<false, false><<<grid, kSimple, 0, s>>>(a);
-  return cudaGetLastError();
+size_t kv_attn_workspace(int sms, int d) {
+  return 256 + (size_t)3 * sms * (sizeof(KvOpen) + 2 * part_floats(d) * sizeof(float));
+}
+
+cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, cudaStream_t s) {
+  const int ctas = line_ctas(sms, a);
+  const KvLine line = carve_line(ws, ctas);
+  const bool sel = a.indices != nullptr;
+  if (a.c.d == 128) {
+    if (a.is_bf16) return sel ? launch_line<128, true, true>(a, ctas, line, s) : launch_line<128, true, false>(a, ctas, line, s);
+    return sel ? launch_line<128, false, true>(a, ctas, line, s) : launch_line<128, false, false>(a, ctas, line, s);
+  }
+  if (a.is_bf16) return sel ? launch_line<64, true, true>(a, ctas, line, s) : launch_line<64, true, false>(a, ctas, line, s);
+  return sel ? launch_line<64, false, true>(a, ctas, line, s) : launch_line<64, false, false>(a, ctas, line, s);
 }
 
 }  // namespace pivot
