@@ -2,6 +2,7 @@
 // them, e4m3 conversions and the search for a row's sequence.
 #pragma once
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -56,8 +57,31 @@ struct KvAttnArgs {
 };
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t s);
+// What a CTA leaves for the merge when it began an item that others end.  The work of an attention call is a line
+// of tiles, item after item, of which every CTA takes an equal stretch.
+struct alignas(16) KvOpen {
+  int64_t item_end, total;  // in tiles of the line
+  int64_t row0;             // first query row's index
+  int32_t stretch, cta_count, head0, rr0, valid, open;
+};
+
+struct KvLine {
+  int* status;
+  const int* gate;  // null, or: run only where it is not 0
+  KvOpen* open;     // [ctas]
+  float* part;      // [ctas][2][kv_part_floats]: of an item that the stretch ends, of one that it begins
+};
+
+// Partial result of an item of `rows` query rows: sums [rows][d], then (m', m, l, 0) of each row.
+__host__ __device__ constexpr size_t kv_part_floats(int rows, int d) { return (size_t)rows * (d + 4); }
+
 size_t kv_attn_workspace(int sms, int d);
-cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, cudaStream_t s);
+cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, const int* gate, cudaStream_t s);
+cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, int split, float lift,
+                            cudaStream_t s);
+size_t kv_attn_tc_workspace(int sms, int d);
+cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms, void* ws,
+                              uint64_t timeout_ns, cudaStream_t s);
 
 // The sequence b with off[b] <= r < off[b+1], or -1.
 __device__ __forceinline__ int kv_sequence_of(const KvStep& st, int64_t r) {
@@ -69,6 +93,23 @@ __device__ __forceinline__ int kv_sequence_of(const KvStep& st, int64_t r) {
     else hi = mid;
   }
   return lo;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {  // two e4m3 bytes to two fp16
+  uint32_t r;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 h = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 // The page of a position below 2^31, or -1 where it is absent.

@@ -52,6 +52,32 @@ int sms() {
   return n;
 }
 
+// The payload as rows of 128 bytes, in boxes of one block's 16 tokens, 128-byte swizzle.
+bool payload_map(CUtensorMap* m, const void* base, int64_t rows) {
+  typedef CUresult (*Fn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                         const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                         CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static Fn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    return cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+                   q == cudaDriverEntryPointSuccess
+               ? reinterpret_cast<Fn>(p)
+               : nullptr;
+  }();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {128, (cuuint64_t)rows}, strides[1] = {128};
+  const cuuint32_t box[2] = {128, PIVOT_KV_BLOCK}, each[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, each,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Whether a call goes to the tcgen05 kernel.
+bool many_rows(int64_t rows, int B, int q_heads, int kv_heads, int d, pivot_dtype dt) {
+  return dt == PIVOT_BF16 && d == 128 && rows * (q_heads / kv_heads) > 16 * (int64_t)B;
+}
+
 // Checks that the attention calls share, and the argument block they launch with.
 pivot_status attention_args(const pivot_kv_cache* cache, const pivot_kv_step* step, const void* q, int64_t q_stride,
                             int q_heads, pivot_dtype dt, float scale, void* out, void* ws, KvAttnArgs* a) {
@@ -130,7 +156,8 @@ size_t pivot_kv_workspace_size(int64_t rows, int B, int q_heads, int kv_heads, i
   if (rows < 0 || rows >= 0x7FFFFFF0ll || B <= 0 || kv_heads <= 0 || q_heads <= 0 || q_heads > 1024 ||
       q_heads % kv_heads || (d != 64 && d != 128) || topk < 0 || topk > 65536 || (dt != PIVOT_BF16 && dt != PIVOT_F32))
     return 0;
-  return kv_attn_workspace(sms(), d);
+  return topk == 0 && many_rows(rows, B, q_heads, kv_heads, d, dt) ? kv_attn_tc_workspace(sms(), d)
+                                                                 : kv_attn_workspace(sms(), d);
 }
 
 pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step* step, const void* q,
@@ -148,7 +175,17 @@ pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step
   a.window = window;
   a.sinks = sinks;
   if (step->rows == 0) return PIVOT_OK;
-  const cudaError_t e = launch_kv_attn(a, sms(), ws, reinterpret_cast<cudaStream_t>(stream));
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  cudaError_t e;
+  if (many_rows(step->rows, step->B, q_heads, cache->kv_heads, cache->d, dt)) {
+    const int64_t slots = (int64_t)cache->num_pages * cache->kv_heads * cache->page_size;
+    CUtensorMap kmap, vmap;
+    if (!payload_map(&kmap, cache->k, slots) || !payload_map(&vmap, cache->v, slots))
+      return record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+    e = launch_kv_attn_tc(a, kmap, vmap, sms(), ws, device_timeout_ns(), s);
+  } else {
+    e = launch_kv_attn(a, sms(), ws, nullptr, s);
+  }
   return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv attention kernel");
 }
 
@@ -169,7 +206,7 @@ pivot_status pivot_kv_attention_selected(const pivot_kv_cache* cache, const pivo
   a.idx_stride = index_stride;
   a.topk = topk;
   if (step->rows == 0) return PIVOT_OK;
-  const cudaError_t e = launch_kv_attn(a, sms(), ws, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv_attn(a, sms(), ws, nullptr, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv selected attention kernel");
 }
 

@@ -16,8 +16,6 @@
 // Work is cut evenly whatever the lengths are: all tiles of 128 tokens of all (sequence, key head, 16 query rows)
 // stand in one line, and every CTA takes an equal stretch of it.  A stretch that begins or ends inside an item
 // leaves a partial result, which kv_merge_kernel joins in a fixed order.
-#include <cuda_fp16.h>
-
 #include "kv.cuh"
 
 namespace pivot {
@@ -29,43 +27,11 @@ constexpr int kWTok = 32;               // tokens a warp takes at a time (two bl
 constexpr int kTile = kWTok * kWarps;   // tokens of a tile
 constexpr float kLift = 14.f;           // weights stand 2^14 above the largest term: fp16 keeps 11 bits down to 2^-28
 
-// What a CTA leaves for the merge when it began an item that others end.
-struct alignas(16) KvOpen {
-  int64_t item_end, total;  // in tiles of the line
-  int64_t row0;             // first query row's index
-  int32_t stretch, cta_count, head0, rr0, valid, open;
-};
-
-__host__ __device__ constexpr size_t part_floats(int d) { return (size_t)kRowsT * (d + 4); }  // o, then m', m, l, 0
-
-struct KvLine {
-  KvOpen* open;   // [ctas]
-  float* part;    // [ctas][2][part_floats]
-  int* status;
-};
-
-__device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {
-  uint32_t r;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-  return r;
-}
-
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
-  const __half2 h = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 __device__ __forceinline__ float quad_max(float x) {
@@ -135,7 +101,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, tig = lane % 4;
   float* const stats = reinterpret_cast<float*>(smem + S::kRing + S::kQBytes);  // [warp][16 rows][m', m, l]
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
-  if (blockIdx.x == 0 && tid == 0) *line.status = 0;
+  if (line.gate) {
+    if (*line.gate == 0) return;
+  } else if (blockIdx.x == 0 && tid == 0) {
+    *line.status = 0;
+  }
 
   // this CTA's stretch of the line
   int64_t total = 0, sel_rows = 0;
@@ -606,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
     }
     __syncthreads();
     const bool all = t0 == 0 && t1 == e.tiles;
-    float* const part = line.part + ((int64_t)blockIdx.x * 2 + (t0 == 0)) * part_floats(D);
+    float* const part = line.part + ((int64_t)blockIdx.x * 2 + (t0 == 0)) * kv_part_floats(kRowsT, D);
     constexpr int kLanes = D / 4;  // threads of a row
     for (int r = tid / kLanes; r < valid; r += kThreads / kLanes) {
       const int c = tid % kLanes * 4;
@@ -662,9 +632,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 // every eighth of them, lanes four dims; the order of the sums is fixed by the line alone.
 constexpr int kMergeWarps = 8;
 template <int D, bool BF16>
-__global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvAttnArgs a, const KvLine line) {
+__global__ void __launch_bounds__(32 * kMergeWarps)
+    kv_merge_kernel(const KvAttnArgs a, const KvLine line, const int rows, const float lift) {
   __shared__ float sums[kMergeWarps][D + 4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (line.gate && *line.gate == 0) return;
   const KvOpen op = line.open[blockIdx.x];
   if (!op.open) return;
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -680,12 +652,12 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvAttn
     more = (int)(lo - op.stretch);
   }
   auto part_of = [&](int i) {  // the first one stands in the place of an item begun, the others in that of one ended
-    return line.part + ((int64_t)(op.stretch + i) * 2 + (i == 0)) * part_floats(D);
+    return line.part + ((int64_t)(op.stretch + i) * 2 + (i == 0)) * kv_part_floats(rows, D);
   };
   for (int r = blockIdx.y; r < op.valid; r += gridDim.y) {
     float mp = -INFINITY, m = -INFINITY;
     for (int i = lane; i <= more; i += 32) {
-      const float4 s = *reinterpret_cast<const float4*>(part_of(i) + kRowsT * D + r * 4);
+      const float4 s = *reinterpret_cast<const float4*>(part_of(i) + rows * D + r * 4);
       mp = fmaxf(mp, s.x);
       m = fmaxf(m, s.y);
     }
@@ -700,7 +672,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvAttn
 #pragma unroll 4
     for (int i = warp; i <= more; i += kMergeWarps) {
       const float* p = part_of(i);
-      const float4 s = *reinterpret_cast<const float4*>(p + kRowsT * D + r * 4);
+      const float4 s = *reinterpret_cast<const float4*>(p + rows * D + r * 4);
       l += s.y == -INFINITY ? s.z : s.z * ex2(s.y - m);
       const float f = s.x == -INFINITY ? (s.z == 0.f ? 0.f : 1.f) : ex2(s.x - mp);
       if (mine) {
@@ -724,7 +696,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) kv_merge_kernel(const KvAttn
       const int64_t row = op.row0 + (op.rr0 + r) / a.group;
       if (row < a.st.rows) {
         const int j = op.head0 + (op.rr0 + r) % a.group;
-        const float f = lt == 0.f ? 0.f : ex2(mp - m - kLift) / lt;
+        const float f = lt == 0.f ? 0.f : ex2(mp - m - lift) / lt;
         if (mine) kv_store4(a, (row * a.hq + j) * (int64_t)D + lane * 4, acc.x * f, acc.y * f, acc.z * f, acc.w * f, BF16);
         if (a.lse && lane == 0) a.lse[row * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(lt));
       }
@@ -767,8 +739,19 @@ cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaS
   if (e != cudaSuccess || ctas == 1) return e;
   // Few items cut into many parts: one block for each row of an item, so that a long join has 16 of them.
   const int64_t items = a.indices ? a.st.rows * a.c.hk : (a.st.B + a.st.rows * a.group / kRowsT) * (int64_t)a.c.hk;
+  return launch_kv_merge(a, line, ctas, kRowsT, ctas > 4 * items ? kRowsT : 2, kLift, s);
+}
+
+}  // namespace
+
+size_t kv_attn_workspace(int sms, int d) {
+  return 256 + (size_t)3 * sms * (sizeof(KvOpen) + 2 * kv_part_floats(kRowsT, d) * sizeof(float));
+}
+
+cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, int split, float lift,
+                            cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, ctas > 4 * items ? kRowsT : 2);
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)split);
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -776,18 +759,17 @@ cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaS
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kv_merge_kernel<D, BF16>, a, line);
+  if (a.c.d == 128)
+    return a.is_bf16 ? cudaLaunchKernelEx(&cfg, kv_merge_kernel<128, true>, a, line, rows, lift)
+                     : cudaLaunchKernelEx(&cfg, kv_merge_kernel<128, false>, a, line, rows, lift);
+  return a.is_bf16 ? cudaLaunchKernelEx(&cfg, kv_merge_kernel<64, true>, a, line, rows, lift)
+                   : cudaLaunchKernelEx(&cfg, kv_merge_kernel<64, false>, a, line, rows, lift);
 }
 
-}  // namespace
-
-size_t kv_attn_workspace(int sms, int d) {
-  return 256 + (size_t)3 * sms * (sizeof(KvOpen) + 2 * part_floats(d) * sizeof(float));
-}
-
-cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, cudaStream_t s) {
+cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, const int* gate, cudaStream_t s) {
   const int ctas = line_ctas(sms, a);
-  const KvLine line = carve_line(ws, ctas);
+  KvLine line = carve_line(ws, ctas);
+  line.gate = gate;
   const bool sel = a.indices != nullptr;
   if (a.c.d == 128) {
     if (a.is_bf16) return sel ? launch_line<128, true, true>(a, ctas, line, s) : launch_line<128, true, false>(a, ctas, line, s);

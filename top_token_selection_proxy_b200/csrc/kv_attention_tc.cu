@@ -1,0 +1,705 @@
+// kv_attention_tc.cu -- attention over the paged 8-bit cache with many query rows for a key head (a group of draft
+// tokens of many heads, a chunk of a prompt): bf16 queries, d = 128, on the tcgen05 tensor cores.
+//
+// The same sums as kv_attention.cu (two running maxima, one for the denominator and one for the numerator with the
+// values' scales), for items of 128 query rows by tiles of 128 tokens:
+//   S = Q K^T   kind::f8f6f4.  Keys are multiplied as they lie in the cache: TMA brings e4m3 pages into the swizzled
+//               operand layout, nothing is converted.  A bf16 query has 8 bits: two e4m3 parts of 4 bits hold it
+//               (scaled to 2^8; what lies 2^-10 below a row's largest keeps fewer), two products into one sum.
+//   O += P V    kind::f16.  Weights leave the softmax as fp16 and stay in tensor memory, where S was; four warps
+//               turn the values into fp16.
+// Two tiles are in work at a time, each with its own S, O and softmax warpgroup: while one is in the softmax, the
+// tensor core multiplies for the other.  Both results are joined at the item's end.
+//
+// What bounds it: the exponentials (16 a clock and SM: 1024 clocks a tile) and the products (1024 clocks) for full
+// items; with half the rows or fewer the cache's bytes.
+#include "kv.cuh"
+
+namespace pivot {
+namespace {
+
+constexpr int D = 128, M = 128, kTok = 128;
+constexpr int kKS = 4, kVS = 3, kMeta = 8;   // stages of keys, of raw values, of the blocks' scales
+constexpr int kTileB = kTok * D;             // bytes of an e4m3 tile
+constexpr int kSoft = 256, kConv = 128;      // threads: two softmax warpgroups, one of the converters
+constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWMma = kWTma + 1;
+constexpr int kThreads = 32 * (kWMma + 1);
+constexpr float kLift = 7.f, kSlack = 8.f;   // weights up to 2^(7+8): the maxima may lag by 2^8 before sums are rescaled
+
+struct Meta {  // of a tile's 8 blocks
+  float ks[8], ve[8], iv[8];  // 2^ke, ve, 2^-ve
+  uint32_t present;           // one bit a block
+  uint32_t pad[7];
+};
+
+struct Tail {
+  uint64_t kf[kKS], ke[kKS], vf[kVS], ve[kVS], hf[2], he[2], sf[2], pf[2], mf[kMeta], qf, of, xf;
+  uint32_t tmem_slot;
+  volatile int abort_flag;
+  Meta meta[kMeta];
+  float unit[M];
+  float stats[2][M][3];
+};
+
+constexpr int kOffQ = 0, kOffK = 2 * M * D, kOffV = kOffK + kKS * kTileB, kOffH = kOffV + kVS * kTileB,
+              kOffTail = kOffH + 2 * kTok * D * 2;
+constexpr size_t kSmem = kOffTail + sizeof(Tail);
+static_assert(kSmem <= 232448, "227 KB of dynamic shared memory per CTA");
+
+struct TcArgs {
+  KvAttnArgs a;
+  KvLine line;
+  int* gate;            // set where a masked place holds a NaN value
+  int64_t slots;        // rows of the cache's tensor maps
+  uint64_t timeout_ns;
+};
+
+// ---------------------------------------------------------------- items: 128 query rows of a sequence and key head
+struct Item {
+  int b, h, rt, row_tiles;
+  int64_t row0, first, p_lo, p_hi;  // first row's index; positions of the sequence's first row, of the item's
+  int hi, rr0, valid;               // last position there is; first query row, how many
+  int ahead, w0, tiles;             // tiles of the first tokens, first tile after them, all
+  __device__ int tile(int k) const { return k < ahead ? k : w0 + k - ahead; }
+};
+
+struct Seq {
+  int64_t row0, first;
+  int hi, row_tiles;
+  int64_t n;
+};
+
+__device__ __forceinline__ Seq seq_of(const KvAttnArgs& a, int b) {
+  Seq s{};
+  if (b >= a.st.B) return s;
+  s.row0 = a.st.off[b];
+  s.n = max64(a.st.off[b + 1] - s.row0, 0);
+  const int64_t len = a.st.lens[b];
+  s.first = len - s.n;
+  s.hi = (int)max64(min64(len, (int64_t)a.st.width * a.c.ps) - 1, -1);
+  s.row_tiles = (int)((s.n * a.group + M - 1) / M);
+  return s;
+}
+
+// Which tiles item rt of a sequence reads: those of the first tokens, then from w0 to its last position.
+__device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Seq& s, int rt, Item* it = nullptr) {
+  const int64_t rr0 = (int64_t)rt * M;
+  const int valid = (int)min64(M, s.n * a.group - rr0);
+  const int64_t p_lo = s.first + rr0 / a.group, p_hi = s.first + (rr0 + valid - 1) / a.group;
+  const int64_t last = min64(p_hi, s.hi);
+  int ahead = 0, w0 = 0, tiles = 1;
+  if (last >= 0) {
+    const int lt = (int)(last / kTok);
+    if (a.window > 0) {
+      ahead = min((int)((min64(a.sinks, s.hi + 1) + kTok - 1) / kTok), lt + 1);
+      w0 = max(ahead, (int)(min64(max64(p_lo - a.window + 1, 0), last) / kTok));
+      tiles = ahead + max(lt - w0 + 1, 0);
+    } else {
+      tiles = lt + 1;
+    }
+  }
+  if (it) {
+    it->rt = rt;
+    it->row_tiles = s.row_tiles;
+    it->row0 = s.row0;
+    it->first = s.first;
+    it->hi = s.hi;
+    it->rr0 = (int)rr0;
+    it->valid = valid;
+    it->p_lo = p_lo;
+    it->p_hi = p_hi;
+    it->ahead = ahead;
+    it->w0 = w0;
+    it->tiles = tiles;
+  }
+  return tiles;
+}
+
+// Tiles of a sequence and one key head.  `wide`: the warp's lanes share one sequence's items; else a lane has its own.
+__device__ __forceinline__ int64_t seq_tiles(const KvAttnArgs& a, const Seq& s, bool wide, int lane) {
+  int64_t t = 0;
+  for (int rt = wide ? lane : 0; rt < s.row_tiles; rt += wide ? 32 : 1) t += tiles_of(a, s, rt);
+  if (wide) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+  }
+  return t;
+}
+
+// The CTA's stretch of the line, walked by every role for itself (all lanes of a warp together).
+struct Walk {
+  int64_t at, stop, total, ctas;
+  Item it;
+  Seq s;
+  int t0, t1;  // tiles of the item in the stretch
+  bool live;
+
+  // tiles of 32 sequences, one a lane
+  __device__ int64_t weights(const KvAttnArgs& a, int b0, int lane) const {
+    const Seq q = seq_of(a, b0 + lane);
+    int64_t mine = 0;
+    unsigned many = __ballot_sync(~0u, q.row_tiles > 8);
+    if (q.row_tiles <= 8) mine = seq_tiles(a, q, false, lane);
+    while (many) {
+      const int l = __ffs(many) - 1;
+      many &= many - 1;
+      const int64_t t = seq_tiles(a, seq_of(a, b0 + l), true, lane);
+      if (lane == l) mine = t;
+    }
+    return mine * a.c.hk;
+  }
+
+  __device__ void start(const KvAttnArgs& a, int lane) {
+    total = 0;
+    live = false;
+    for (int b0 = 0; b0 < a.st.B; b0 += 32) total += weights(a, b0, lane);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
+    ctas = min64(gridDim.x, total);
+    if (blockIdx.x >= ctas) return;
+    at = total * blockIdx.x / ctas;
+    stop = total * (blockIdx.x + 1) / ctas;
+    int64_t run = 0;
+    for (int b0 = 0; b0 < a.st.B; b0 += 32) {
+      const int64_t w = weights(a, b0, lane);
+      int64_t inc = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(~0u, inc, o);
+        if (lane >= o) inc += up;
+      }
+      const unsigned hit = __ballot_sync(~0u, run + inc > at);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        int64_t in = at - run - __shfl_sync(~0u, inc - w, l);
+        const int64_t per = __shfl_sync(~0u, w, l) / a.c.hk;
+        it.b = b0 + l;
+        it.h = (int)(in / per);
+        in -= it.h * per;
+        s = seq_of(a, it.b);
+        for (int r0 = 0; r0 < s.row_tiles; r0 += 32) {  // the item: prefix over its sequence's row tiles
+          const int64_t v = r0 + lane < s.row_tiles ? tiles_of(a, s, r0 + lane) : 0;
+          int64_t pre = v;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int64_t up = __shfl_up_sync(~0u, pre, o);
+            if (lane >= o) pre += up;
+          }
+          const unsigned here = __ballot_sync(~0u, pre > in);
+          if (here) {
+            const int k = __ffs(here) - 1;
+            tiles_of(a, s, r0 + k, &it);
+            t0 = (int)(in - __shfl_sync(~0u, pre - v, k));
+            t1 = (int)min64(it.tiles, t0 + (stop - at));
+            live = true;
+            return;
+          }
+          in -= __shfl_sync(~0u, pre, 31);
+        }
+        return;  // only where the lengths changed under the call
+      }
+      run += __shfl_sync(~0u, inc, 31);
+    }
+  }
+
+  __device__ void next(const KvAttnArgs& a) {
+    at += t1 - t0;
+    if (at >= stop) {
+      live = false;
+      return;
+    }
+    int rt = it.rt + 1;
+    if (rt == s.row_tiles) {
+      rt = 0;
+      if (++it.h == a.c.hk) {
+        it.h = 0;
+        do {
+          if (++it.b >= a.st.B) {
+            live = false;
+            return;
+          }
+          s = seq_of(a, it.b);
+        } while (s.row_tiles == 0);
+      }
+    }
+    tiles_of(a, s, rt, &it);
+    t0 = 0;
+    t1 = (int)min64(it.tiles, stop - at);
+  }
+};
+
+// Whether every row of the item sees every token of a tile (where its pages are present).
+__device__ __forceinline__ bool whole_tile(const KvAttnArgs& a, const Item& it, int base) {
+  return base + kTok - 1 <= min64(it.p_lo, it.hi) &&
+         (a.window <= 0 || base > it.p_hi - a.window || base + kTok <= a.sinks);
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    kv_attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                      const TcArgs args) {
+  const KvAttnArgs& a = args.a;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Tail& T = *reinterpret_cast<Tail*>(smem + kOffTail);
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled operands need it; there is no room to align
+    if (threadIdx.x == 0) atomicOr(args.line.status, DEV_ERR_BOUNDS);
+    return;
+  }
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (tid == 0) {
+    for (int i = 0; i < kKS; ++i) mbar_init(&T.kf[i], 1), mbar_init(&T.ke[i], 1);
+    for (int i = 0; i < kVS; ++i) mbar_init(&T.vf[i], 1), mbar_init(&T.ve[i], kConv);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&T.hf[i], kConv), mbar_init(&T.he[i], 1);
+      mbar_init(&T.sf[i], 1), mbar_init(&T.pf[i], kSoft / 2);
+    }
+    for (int i = 0; i < kMeta; ++i) mbar_init(&T.mf[i], 1);
+    mbar_init(&T.qf, kSoft);
+    mbar_init(&T.of, 1);
+    mbar_init(&T.xf, kSoft);
+    T.abort_flag = 0;
+    fence_mbar_init();
+    args.line.open[blockIdx.x].open = 0;
+  }
+  if (warp == kWMma) {
+    tmem_alloc(&T.tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = T.tmem_slot;  // S0, S1, O0, O1: 128 columns each
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    if (mbar_wait(bar, parity, args.timeout_ns, &T.abort_flag)) return true;
+    T.abort_flag = 1;
+    atomicOr(args.line.status, DEV_ERR_TIMEOUT);
+    return false;
+  };
+
+  Walk w;
+  w.start(a, lane);
+
+  if (warp == kWTma) {
+    // ------------------------------------------------------------ copies: pages, scales
+    // Lane l looks after block l % 8 of tile l / 8 of four; four tiles' look-ups are under way while the four
+    // before them are copied.
+    uint32_t n = 0;  // tiles so far
+    bool ok = true;
+    for (; w.live && ok; w.next(a)) {
+      const Item& it = w.it;
+      const int nt = w.t1 - w.t0;
+      auto position = [&](int k) {  // of this lane's block in the four tiles from k on; -1: none
+        const int t = k + lane / 8;
+        if (t >= nt) return -1;
+        const int p = it.tile(w.t0 + t) * kTok + lane % 8 * kKvBlock;
+        return p <= it.hi ? p : -1;
+      };
+      auto page_at = [&](int p) { return p < 0 ? -1 : kv_page(a.st, a.c, it.b, (uint32_t)p); };
+      struct Block {
+        int slot;
+        int8_t ke, ve;
+      };
+      auto block_at = [&](int p, int page) {
+        Block r{-1, 0, 0};
+        if (page >= 0) {
+          const int in = (int)((uint32_t)p % (uint32_t)a.c.ps);
+          const int ph = page * a.c.hk + it.h;
+          r.slot = ph * a.c.ps + in;
+          const int64_t e = (int64_t)ph * (a.c.ps / kKvBlock) + in / kKvBlock;
+          r.ke = __ldg(a.c.ke + e);
+          r.ve = __ldg(a.c.ve + e);
+        }
+        return r;
+      };
+      int p1 = position(0);
+      Block now = block_at(p1, page_at(p1)), then;
+      p1 = position(4);
+      int page1 = page_at(p1);
+      for (int k = 0; k < nt; ++k, ++n) {
+        if (k % 4 == 0) {
+          if (k) now = then;
+          then = block_at(p1, page1);
+          p1 = position(k + 8);
+          page1 = page_at(p1);
+        }
+        const int ks = n % kKS, vs = n % kVS, ms = n % kMeta;
+        int good = 1;
+        if (lane == 0) good = wait(&T.ke[ks], (n / kKS & 1) ^ 1) && wait(&T.ve[vs], (n / kVS & 1) ^ 1);
+        good = __shfl_sync(~0u, good, 0);
+        if (!good) {
+          ok = false;
+          break;
+        }
+        const bool mine = lane / 8 == k % 4;
+        const unsigned there = __ballot_sync(~0u, mine && now.slot >= 0);
+        if (mine) {
+          Meta& m = T.meta[ms];
+          const int i = lane % 8;
+          m.ks[i] = kv_scale(now.ke);
+          m.ve[i] = (float)now.ve;
+          m.iv[i] = kv_exp2i(min(-(int)now.ve, 127));
+          if (i == 0) m.present = there >> (8 * (k % 4)) & 0xFFu;
+        }
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&T.mf[ms]);
+          mbar_arrive_expect_tx(&T.kf[ks], kTileB);
+          mbar_arrive_expect_tx(&T.vf[vs], kTileB);
+        }
+        __syncwarp();
+        if (mine) {
+          const int y = now.slot >= 0 ? now.slot : (int)args.slots;  // behind the last row: zeros
+          const int at = lane % 8 * kKvBlock * D;
+          tma_load_2d(smem + kOffK + ks * kTileB + at, &kmap, &T.kf[ks], 0, y);
+          tma_load_2d(smem + kOffV + vs * kTileB + at, &vmap, &T.vf[vs], 0, y);
+        }
+      }
+    }
+  } else if (warp == kWMma) {
+    // ------------------------------------------------------------ products (one thread)
+    uint32_t n = 0, items = 0, seen[2] = {0, 0};  // tiles; items; weights taken, of each half
+    bool ok = true;
+    for (; w.live && ok; w.next(a), ++items) {
+      const int nt = w.t1 - w.t0;
+      if (lane == 0) {
+        const uint32_t qaddr = smem_u32(smem + kOffQ);
+        auto second = [&](int k) {  // O += P V of the item's tile k
+          const uint32_t i = n - (uint32_t)(nt - k);  // n: tiles up to this item's end
+          const int s = k & 1, hb = i & 1;
+          if (!wait(&T.pf[s], seen[s]++ & 1) || !wait(&T.hf[hb], i / 2 & 1)) return false;
+          tc_fence_after();
+          const uint32_t v = smem_u32(smem + kOffH) + hb * (kTok * D * 2);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk)
+            umma_f16_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * kk,
+                        sw128_mnmajor_desc(v + kk * 16 * 128, kTok * 128, 1024), idesc_f16_f32_bmn(M, D),
+                        k >= 2 || kk > 0);
+          umma_commit(&T.he[hb]);
+          return true;
+        };
+        const uint32_t n0 = n;
+        n += nt;
+        ok = wait(&T.qf, items & 1);
+        tc_fence_after();
+        for (int k = 0; k < nt && ok; ++k) {
+          const uint32_t i = n0 + k;
+          const int ks = i % kKS, s = k & 1;
+          ok = wait(&T.kf[ks], i / kKS & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t kaddr = smem_u32(smem + kOffK) + ks * kTileB;
+#pragma unroll
+          for (int part = 1; part >= 0; --part)
+#pragma unroll
+            for (int kk = 0; kk < D / 32; ++kk)
+              umma_f8(tmem + 128 * s, sw128_kmajor_desc(qaddr + part * M * D + kk * 32),
+                      sw128_kmajor_desc(kaddr + kk * 32), idesc_e4m3_f32(M, kTok), part == 0 || kk > 0);
+          umma_commit(&T.ke[ks]);
+          umma_commit(&T.sf[s]);
+          if (k > 0) ok = second(k - 1);
+        }
+        if (ok) ok = second(nt - 1);
+        if (ok) umma_commit(&T.of);
+      }
+      ok = __shfl_sync(~0u, (int)ok, 0);
+    }
+  } else if (warp >= kWConv) {
+    // ------------------------------------------------------------ values to fp16: a thread for a token
+    const int t = tid - kSoft;
+    uint32_t n = 0;
+    bool ok = true;
+    for (; w.live && ok; w.next(a)) {
+      const int nt = w.t1 - w.t0;
+      for (int k = 0; k < nt; ++k, ++n) {
+        const int vs = n % kVS, hb = n & 1;
+        const int base = w.it.tile(w.t0 + k) * kTok;
+        ok = wait(&T.vf[vs], n / kVS & 1) && wait(&T.he[hb], (n / 2 & 1) ^ 1);
+        if (!ok) break;
+        const uint8_t* src = smem + kOffV + vs * kTileB + t * 128;
+        uint8_t* dst = smem + kOffH + hb * (kTok * D * 2) + t * 128;
+        const bool dead = base + t > w.it.hi;  // what lies behind the last token stays out of the product
+        uint32_t odd = 0;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint4 r = *reinterpret_cast<const uint4*>(src + ((c ^ (t & 7)) << 4));
+          if (dead) r = make_uint4(0, 0, 0, 0);
+          const uint32_t x[4] = {r.x, r.y, r.z, r.w};
+          uint32_t y[8];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            odd |= __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            y[2 * j] = cvt_e4m3x2(x[j]);
+            y[2 * j + 1] = cvt_e4m3x2(x[j] >> 16);
+          }
+          uint8_t* half = dst + (c / 4) * (kTok * 128);  // dims 0-63, then 64-127
+          const int c2 = (c % 4) * 2;
+          *reinterpret_cast<uint4*>(half + ((c2 ^ (t & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
+          *reinterpret_cast<uint4*>(half + (((c2 + 1) ^ (t & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+        }
+        // A weight of zero does not hide a NaN: where some rows may not see this token, the call is computed again
+        // by the kernel that goes row by row.
+        if (odd && !whole_tile(a, w.it, base)) *args.gate = 1;
+        fence_proxy_async_smem();
+        mbar_arrive(&T.hf[hb]);
+        mbar_arrive(&T.ve[vs]);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------ softmax: a thread for a row, a warpgroup for a half
+    const int s = warp / 4, r = tid & 127;
+    const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // lane 32 * (warp % 4) in an address' upper half
+    const uint32_t sc = tmem + lanes + 128 * s, oc = tmem + lanes + 256 + 128 * s;
+    uint32_t n = 0, items = 0, mine = 0;  // tiles of both halves; items; tiles of this half
+    bool ok = true;
+    // after a failed wait the loop only keeps the barriers' count
+    for (; w.live; w.next(a), ++items) {
+      const Item& it = w.it;
+      const int nt = w.t1 - w.t0;
+      const int64_t pos = it.first + (it.rr0 + min(r, it.valid - 1)) / a.group;
+      if (s == 0) {  // the query row in two parts
+        const int rr = it.rr0 + r;
+        const int64_t row = it.row0 + rr / a.group;
+        uint4 x[16];
+        const bool have = r < it.valid && row < a.st.rows;
+        const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + row * a.q_stride +
+                              (int64_t)(it.h * a.group + rr % a.group) * D;
+#pragma unroll
+        for (int c = 0; c < 16; ++c)
+          x[c] = have ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < 16; ++c) {
+          const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)), fabsf(__uint_as_float(v[j] & 0xFFFF0000u))));
+        }
+        const bool finite = top <= 3.402823466e38f;
+        const int ex = top > 0.f && finite ? max((int)(__float_as_uint(top) >> 23) - 127 - 7, -100) : 0;
+        const float f = a.scale2 < 0.f ? -kv_exp2i(-ex) : kv_exp2i(-ex);  // largest in [2^7, 2^8)
+        T.unit[r] = finite ? fabsf(a.scale2) * kv_exp2i(ex) : __int_as_float(0x7FC00000);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t w1[4], w2[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {  // 4 dims a word
+            const uint4& q4 = x[2 * c + j / 2];
+            const uint32_t lo = j % 2 ? q4.z : q4.x, hi = j % 2 ? q4.w : q4.y;
+            const float v[4] = {__uint_as_float(lo << 16) * f, __uint_as_float(lo & 0xFFFF0000u) * f,
+                                __uint_as_float(hi << 16) * f, __uint_as_float(hi & 0xFFFF0000u) * f};
+            uint32_t a1 = __nv_cvt_float2_to_fp8x2(make_float2(v[0], v[1]), __NV_SATFINITE, __NV_E4M3);
+            a1 |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2], v[3]), __NV_SATFINITE, __NV_E4M3) << 16;
+            w1[j] = a1;
+            const uint32_t h0 = cvt_e4m3x2(a1), h1 = cvt_e4m3x2(a1 >> 16);
+            const float2 g0 = __half22float2(*reinterpret_cast<const __half2*>(&h0)),
+                         g1 = __half22float2(*reinterpret_cast<const __half2*>(&h1));
+            uint32_t a2 =
+                __nv_cvt_float2_to_fp8x2(make_float2(v[0] - g0.x, v[1] - g0.y), __NV_SATFINITE, __NV_E4M3);
+            a2 |= (uint32_t)__nv_cvt_float2_to_fp8x2(make_float2(v[2] - g1.x, v[3] - g1.y), __NV_SATFINITE, __NV_E4M3)
+                  << 16;
+            w2[j] = a2;
+          }
+          uint8_t* to = smem + kOffQ + r * 128 + ((c ^ (r & 7)) << 4);
+          *reinterpret_cast<uint4*>(to) = make_uint4(w1[0], w1[1], w1[2], w1[3]);
+          *reinterpret_cast<uint4*>(to + M * D) = make_uint4(w2[0], w2[1], w2[2], w2[3]);
+        }
+        fence_proxy_async_smem();
+      }
+      tc_fence_before();  // the item before: its sums have been read
+      mbar_arrive(&T.qf);
+      ok = __all_sync(~0u, ok && wait(&T.qf, items & 1));
+      const float unit = T.unit[r];
+      const bool idle = 32 * (warp % 4) >= it.valid;  // a warp without rows
+      float m = -INFINITY, mp = -INFINITY, l = 0.f;
+      for (int k = s; k < nt; k += 2, ++mine) {
+        const uint32_t i = n + k;
+        const int base = it.tile(w.t0 + k) * kTok;
+        if (!ok) continue;
+        ok = __all_sync(~0u, wait(&T.mf[i % kMeta], i / kMeta & 1) && wait(&T.sf[s], mine & 1));
+        if (!ok) continue;
+        tc_fence_after();
+        if (!idle) {
+          const Meta& me = T.meta[i % kMeta];
+          const uint32_t present = me.present;
+          const bool whole = present == 0xFFu && whole_tile(a, it, base);
+          auto hidden = [&](int j) {  // whether this row sees column j
+            const int t = base + j;
+            return !(t <= it.hi && t <= pos && (present >> (j / kKvBlock) & 1) &&
+                     (a.window <= 0 || t > pos - a.window || t < a.sinks));
+          };
+          uint32_t x[32];
+          float top = -INFINITY, topv = -INFINITY;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32x32b_x32(sc + 32 * c, x);
+            tmem_wait_ld();
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float cb = unit * me.ks[2 * c + u];
+              float t = -INFINITY;
+              if (whole) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) t = fmaxf(t, __uint_as_float(x[16 * u + j]));
+                t *= cb;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+                  t = fmaxf(t, hidden(32 * c + 16 * u + j) ? -INFINITY : __uint_as_float(x[16 * u + j]) * cb);
+              }
+              top = fmaxf(top, t);
+              topv = fmaxf(topv, t + me.ve[2 * c + u]);
+            }
+          }
+          if (top > m + kSlack || m == -INFINITY) {
+            l *= m == -INFINITY ? 1.f : ex2(m - top);
+            m = top;
+          }
+          const bool up = topv > mp + kSlack || mp == -INFINITY;
+          const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
+          if (up) mp = topv;
+          if (k >= 2 && __any_sync(~0u, f != 1.f)) {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              tmem_ld32x32b_x32(oc + 32 * c, x);
+              tmem_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
+              tmem_st32x32b_x32(oc + 32 * c, x);
+            }
+          }
+          const float mr = m == -INFINITY ? 0.f : m, mpr = mp == -INFINITY ? 0.f : mp;
+          const float back = ex2(mpr - kLift - mr);  // weights of the product to those of the sum, but for 2^-ve
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tmem_ld32x32b_x32(sc + 32 * c, x);
+            tmem_wait_ld();
+            uint32_t y[16];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float cb = unit * me.ks[2 * c + u], off = me.ve[2 * c + u] - mpr + kLift;
+              float sum = 0.f;
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                float e0, e1;
+                if (whole) {
+                  e0 = ex2(fmaf(__uint_as_float(x[16 * u + j]), cb, off));
+                  e1 = ex2(fmaf(__uint_as_float(x[16 * u + j + 1]), cb, off));
+                } else {
+                  e0 = hidden(32 * c + 16 * u + j) ? 0.f : ex2(fmaf(__uint_as_float(x[16 * u + j]), cb, off));
+                  e1 = hidden(32 * c + 16 * u + j + 1) ? 0.f : ex2(fmaf(__uint_as_float(x[16 * u + j + 1]), cb, off));
+                }
+                sum += e0 + e1;
+                y[8 * u + j / 2] = pack_f16(e0, e1);
+              }
+              l += sum == 0.f ? 0.f : sum * (back * me.iv[2 * c + u]);
+            }
+            tmem_st32x32b_x16(sc + 16 * c, y);
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(&T.pf[s]);
+      }
+      // both halves together: each warpgroup takes half of the dims
+      ok = __all_sync(~0u, ok && wait(&T.of, items & 1));
+      tc_fence_after();
+      T.stats[s][r][0] = mp;
+      T.stats[s][r][1] = m;
+      T.stats[s][r][2] = l;
+      mbar_arrive(&T.xf);
+      ok = __all_sync(~0u, ok && wait(&T.xf, items & 1));
+      if (ok && !idle) {
+        float mps[2], ms[2], ls[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) mps[u] = T.stats[u][r][0], ms[u] = T.stats[u][r][1], ls[u] = T.stats[u][r][2];
+        const float mpt = fmaxf(mps[0], mps[1]), mt = fmaxf(ms[0], ms[1]);
+        float lt = 0.f, f[2];
+        bool use[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          use[u] = !(mps[u] == -INFINITY && ls[u] == 0.f) && u < nt;
+          f[u] = mps[u] == -INFINITY ? 1.f : ex2(mps[u] - mpt);
+          lt += ms[u] == -INFINITY ? ls[u] : ls[u] * ex2(ms[u] - mt);
+        }
+        const bool all = w.t0 == 0 && w.t1 == it.tiles;
+        const float g = all ? (lt == 0.f ? 0.f : ex2(mpt - mt - kLift) / lt) : 1.f;
+        const int rr = it.rr0 + r;
+        const int64_t row = it.row0 + rr / a.group;
+        const int j = it.h * a.group + rr % a.group;
+        const bool put = r < it.valid && row < a.st.rows;
+        float* const part = args.line.part + ((int64_t)blockIdx.x * 2 + (w.t0 == 0)) * kv_part_floats(M, D);
+#pragma unroll 1
+        for (int c = 0; c < 2; ++c) {
+          const int d0 = 64 * s + 32 * c;
+          uint32_t x[32], y[32];
+          tmem_ld32x32b_x32(tmem + lanes + 256 + d0, x);
+          if (nt > 1) tmem_ld32x32b_x32(tmem + lanes + 384 + d0, y);
+          tmem_wait_ld();
+          if (put) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) {
+              float v[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                v[q] = use[0] ? __uint_as_float(x[e + q]) * f[0] : 0.f;
+                if (use[1]) v[q] += __uint_as_float(y[e + q]) * f[1];
+                v[q] *= g;
+              }
+              if (all) kv_store4(a, (row * a.hq + j) * (int64_t)D + d0 + e, v[0], v[1], v[2], v[3], true);
+              else *reinterpret_cast<float4*>(part + r * D + d0 + e) = make_float4(v[0], v[1], v[2], v[3]);
+            }
+          }
+        }
+        if (put && s == 0) {
+          if (all) {
+            if (a.lse) a.lse[row * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (mt + log2f(lt));
+          } else {
+            *reinterpret_cast<float4*>(part + M * D + r * 4) = make_float4(mpt, mt, lt, 0.f);
+          }
+        }
+        if (tid == 0 && !all && w.t0 == 0)
+          args.line.open[blockIdx.x] = {w.at + it.tiles, w.total, it.row0, (int)blockIdx.x, (int)w.ctas,
+                                        it.h * a.group, it.rr0, it.valid, 1};
+      }
+      n += nt;
+    }
+  }
+
+  __syncthreads();
+  if (T.abort_flag) {  // let copies and products in flight end before tensor memory goes
+    const uint64_t t0 = globaltimer_ns();
+    while (globaltimer_ns() - t0 < 200000ull) {
+    }
+  }
+  if (warp == kWMma) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace
+
+size_t kv_attn_tc_workspace(int sms, int d) {
+  return 256 + (size_t)sms * (sizeof(KvOpen) + 2 * kv_part_floats(M, D) * sizeof(float)) + kv_attn_workspace(sms, d);
+}
+
+cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms, void* ws,
+                              uint64_t timeout_ns, cudaStream_t s) {
+  cudaError_t e = cudaMemsetAsync(ws, 0, 256, s);
+  if (e != cudaSuccess) return e;
+  char* p = static_cast<char*>(ws);
+  TcArgs t{};
+  t.a = a;
+  t.line.status = reinterpret_cast<int*>(p);
+  t.gate = reinterpret_cast<int*>(p + 64);
+  t.line.open = reinterpret_cast<KvOpen*>(p + 256);
+  t.line.part = reinterpret_cast<float*>(p + 256 + (size_t)sms * sizeof(KvOpen));
+  t.slots = (int64_t)a.c.pages * a.c.hk * a.c.ps;
+  t.timeout_ns = timeout_ns;
+  e = cudaFuncSetAttribute(kv_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  if (e != cudaSuccess) return e;
+  kv_attn_tc_kernel<<<sms, kThreads, kSmem, s>>>(kmap, vmap, t);
+  e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_kv_merge(a, t.line, sms, M, 16, kLift, s);
+  if (e != cudaSuccess) return e;
+  return launch_kv_attn(a, sms, p + 256 + (size_t)sms * (sizeof(KvOpen) + 2 * kv_part_floats(M, D) * sizeof(float)),
+                        t.gate, s);
+}
+
+}  // namespace pivot
