@@ -32,20 +32,6 @@ struct Meta {  // of a tile's 8 blocks
   uint32_t pad[7];
 };
 
-struct Tail {
-  uint64_t kf[kKS], ke[kKS], vf[kVS], ve[kVS], hf[2], he[2], sf[2], pf[2], mf[kMeta], qf, of, xf;
-  uint32_t tmem_slot;
-  volatile int abort_flag;
-  Meta meta[kMeta];
-  float unit[M];
-  float stats[2][M][3];
-};
-
-constexpr int kOffQ = 0, kOffK = 2 * M * D, kOffV = kOffK + kKS * kTileB, kOffH = kOffV + kVS * kTileB,
-              kOffTail = kOffH + 2 * kTok * D * 2;
-constexpr size_t kSmem = kOffTail + sizeof(Tail);
-static_assert(kSmem <= 232448, "227 KB of dynamic shared memory per CTA");
-
 struct TcArgs {
   KvAttnArgs a;
   KvLine line;
@@ -228,6 +214,34 @@ struct Walk {
   }
 };
 
+struct Tail {
+  uint64_t kf[kKS], ke[kKS], vf[kVS], ve[kVS], hf[2], he[2], sf[2], pf[2], mf[kMeta], qf, of, xf;
+  uint32_t tmem_slot;
+  volatile int abort_flag;
+  Meta meta[kMeta];
+  Walk walk[kWMma + 1];  // one for each warp: in registers it would crowd out the softmax
+  float unit[M];
+  float stats[2][M][3];
+};
+
+constexpr int kOffQ = 0, kOffK = 2 * M * D, kOffV = kOffK + kKS * kTileB, kOffH = kOffV + kVS * kTileB,
+              kOffTail = kOffH + 2 * kTok * D * 2;
+constexpr size_t kSmem = kOffTail + sizeof(Tail);
+static_assert(kSmem <= 232448, "227 KB of dynamic shared memory per CTA");
+
+// 2^x without the special-function unit, for x < 127: 2^r of r = x - round(x) in [-1/2, 1/2] by a polynomial that
+// interpolates it at the five Chebyshev points (relative error below 4e-6), times 2^round(x).
+__device__ __forceinline__ float ex2_fma(float x) {
+  const float c = x < -126.f ? -126.f : x;
+  const float t = c + 12582912.f;  // 1.5 * 2^23: the low bits hold round(c)
+  const float r = c - (t - 12582912.f);
+  float p = fmaf(0.00966636837f, r, 0.0559219755f);
+  p = fmaf(p, r, 0.240223497f);
+  p = fmaf(p, r, 0.693121016f);
+  p = fmaf(p, r, 1.f);
+  return p * __int_as_float((__float_as_int(t) << 23) + 0x3F800000);  // a product, so that NaN stays NaN
+}
+
 // Whether every row of the item sees every token of a tile (where its pages are present).
 __device__ __forceinline__ bool whole_tile(const KvAttnArgs& a, const Item& it, int base) {
   return base + kTok - 1 <= min64(it.p_lo, it.hi) &&
@@ -275,8 +289,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     return false;
   };
 
-  Walk w;
-  w.start(a, lane);
+  Walk& w = T.walk[warp];
+  {
+    Walk v;
+    v.start(a, lane);
+    if (lane == 0) w = v;
+    __syncwarp();
+  }
+  auto advance = [&]() {
+    __syncwarp();
+    if (lane == 0) w.next(a);
+    __syncwarp();
+  };
 
   if (warp == kWTma) {
     // ------------------------------------------------------------ copies: pages, scales
@@ -284,7 +308,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // before them are copied.
     uint32_t n = 0;  // tiles so far
     bool ok = true;
-    for (; w.live && ok; w.next(a)) {
+    for (; w.live && ok; advance()) {
       const Item& it = w.it;
       const int nt = w.t1 - w.t0;
       auto position = [&](int k) {  // of this lane's block in the four tiles from k on; -1: none
@@ -358,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ products (one thread)
     uint32_t n = 0, items = 0, seen[2] = {0, 0};  // tiles; items; weights taken, of each half
     bool ok = true;
-    for (; w.live && ok; w.next(a), ++items) {
+    for (; w.live && ok; advance(), ++items) {
       const int nt = w.t1 - w.t0;
       if (lane == 0) {
         const uint32_t qaddr = smem_u32(smem + kOffQ);
@@ -407,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int t = tid - kSoft;
     uint32_t n = 0;
     bool ok = true;
-    for (; w.live && ok; w.next(a)) {
+    for (; w.live && ok; advance()) {
       const int nt = w.t1 - w.t0;
       for (int k = 0; k < nt; ++k, ++n) {
         const int vs = n % kVS, hb = n & 1;
@@ -417,6 +441,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint8_t* src = smem + kOffV + vs * kTileB + t * 128;
         uint8_t* dst = smem + kOffH + hb * (kTok * D * 2) + t * 128;
         const bool dead = base + t > w.it.hi;  // what lies behind the last token stays out of the product
+        const bool look = !whole_tile(a, w.it, base);
         uint32_t odd = 0;
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
@@ -426,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           uint32_t y[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            odd |= __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            if (look) odd |= __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
             y[2 * j] = cvt_e4m3x2(x[j]);
             y[2 * j + 1] = cvt_e4m3x2(x[j] >> 16);
           }
@@ -437,7 +462,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // A weight of zero does not hide a NaN: where some rows may not see this token, the call is computed again
         // by the kernel that goes row by row.
-        if (odd && !whole_tile(a, w.it, base)) *args.gate = 1;
+        if (odd) *args.gate = 1;
         fence_proxy_async_smem();
         mbar_arrive(&T.hf[hb]);
         mbar_arrive(&T.ve[vs]);
@@ -451,38 +476,40 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t n = 0, items = 0, mine = 0;  // tiles of both halves; items; tiles of this half
     bool ok = true;
     // after a failed wait the loop only keeps the barriers' count
-    for (; w.live; w.next(a), ++items) {
+    for (; w.live; advance(), ++items) {
       const Item& it = w.it;
       const int nt = w.t1 - w.t0;
       const int64_t pos = it.first + (it.rr0 + min(r, it.valid - 1)) / a.group;
       if (s == 0) {  // the query row in two parts
         const int rr = it.rr0 + r;
         const int64_t row = it.row0 + rr / a.group;
-        uint4 x[16];
         const bool have = r < it.valid && row < a.st.rows;
         const uint16_t* src = reinterpret_cast<const uint16_t*>(a.q) + row * a.q_stride +
                               (int64_t)(it.h * a.group + rr % a.group) * D;
-#pragma unroll
-        for (int c = 0; c < 16; ++c)
-          x[c] = have ? *reinterpret_cast<const uint4*>(src + 8 * c) : make_uint4(0, 0, 0, 0);
+        auto load = [&](int c) {
+          return have ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+        };
         float top = 0.f;
-#pragma unroll
+#pragma unroll 8
         for (int c = 0; c < 16; ++c) {
-          const uint32_t v[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+          const uint4 x = load(c);
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[j] << 16)), fabsf(__uint_as_float(v[j] & 0xFFFF0000u))));
         }
         const bool finite = top <= 3.402823466e38f;
         const int ex = top > 0.f && finite ? max((int)(__float_as_uint(top) >> 23) - 127 - 7, -100) : 0;
-        const float f = a.scale2 < 0.f ? -kv_exp2i(-ex) : kv_exp2i(-ex);  // largest in [2^7, 2^8)
-        T.unit[r] = finite ? fabsf(a.scale2) * kv_exp2i(ex) : __int_as_float(0x7FC00000);
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        const float f = !finite ? __int_as_float(0x7FC00000)  // e4m3 has no infinity: such a row is NaN
+                        : a.scale2 < 0.f ? -kv_exp2i(-ex) : kv_exp2i(-ex);  // largest in [2^7, 2^8)
+        T.unit[r] = fabsf(a.scale2) * kv_exp2i(ex);
+#pragma unroll 2
+        for (int c = 0; c < 8; ++c) {  // read again: 128 dims would not stay in registers
+          const uint4 x[2] = {load(2 * c), load(2 * c + 1)};
           uint32_t w1[4], w2[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {  // 4 dims a word
-            const uint4& q4 = x[2 * c + j / 2];
+            const uint4& q4 = x[j / 2];
             const uint32_t lo = j % 2 ? q4.z : q4.x, hi = j % 2 ? q4.w : q4.y;
             const float v[4] = {__uint_as_float(lo << 16) * f, __uint_as_float(lo & 0xFFFF0000u) * f,
                                 __uint_as_float(hi << 16) * f, __uint_as_float(hi & 0xFFFF0000u) * f};
@@ -521,76 +548,101 @@ __global__ void __launch_bounds__(kThreads, 1)
           const Meta& me = T.meta[i % kMeta];
           const uint32_t present = me.present;
           const bool whole = present == 0xFFu && whole_tile(a, it, base);
-          auto hidden = [&](int j) {  // whether this row sees column j
-            const int t = base + j;
-            return !(t <= it.hi && t <= pos && (present >> (j / kKvBlock) & 1) &&
-                     (a.window <= 0 || t > pos - a.window || t < a.sinks));
+          // which of 32 columns this row sees, where the tile is not whole
+          const int upto = (int)max64(min64(min64(it.hi, pos) - base + 1, kTok), 0);
+          const int from = a.window > 0 ? (int)max64(min64(pos - a.window + 1 - base, kTok), 0) : 0;
+          const int sinks = a.window > 0 ? (int)max64(min64(a.sinks - base, kTok), 0) : 0;
+          auto seen = [&](int c) {
+            auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+            const uint32_t there = ((present >> (2 * c) & 1) ? 0xFFFFu : 0u) | ((present >> (2 * c + 1) & 1) ? 0xFFFF0000u : 0u);
+            return below(upto - 32 * c) & (~below(from - 32 * c) | below(sinks - 32 * c)) & there;
           };
-          uint32_t x[32];
-          float top = -INFINITY, topv = -INFINITY;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tmem_ld32x32b_x32(sc + 32 * c, x);
-            tmem_wait_ld();
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float cb = unit * me.ks[2 * c + u];
-              float t = -INFINITY;
-              if (whole) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) t = fmaxf(t, __uint_as_float(x[16 * u + j]));
-                t *= cb;
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                  t = fmaxf(t, hidden(32 * c + 16 * u + j) ? -INFINITY : __uint_as_float(x[16 * u + j]) * cb);
-              }
-              top = fmaxf(top, t);
-              topv = fmaxf(topv, t + me.ve[2 * c + u]);
-            }
-          }
-          if (top > m + kSlack || m == -INFINITY) {
-            l *= m == -INFINITY ? 1.f : ex2(m - top);
-            m = top;
-          }
-          const bool up = topv > mp + kSlack || mp == -INFINITY;
-          const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
-          if (up) mp = topv;
-          if (k >= 2 && __any_sync(~0u, f != 1.f)) {
+          // One pass over S, 32 columns at a time.  The weights' reference m' (and m, the sum's) may lag behind the
+          // largest score by 2^8; where it would by more, what was weighed with the old one is scaled down: the
+          // output sums, and this tile's weights so far.  After the first columns of an item that is rare.
+          // The loop is not unrolled: its code then stays in the instruction cache (unrolled it ran at half the speed).
+          float mpr = mp == -INFINITY ? 0.f : mp;
+          float back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));  // product's weights to the sum's, but for 2^-ve
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              tmem_ld32x32b_x32(oc + 32 * c, x);
-              tmem_wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * f);
-              tmem_st32x32b_x32(oc + 32 * c, x);
-            }
-          }
-          const float mr = m == -INFINITY ? 0.f : m, mpr = mp == -INFINITY ? 0.f : mp;
-          const float back = ex2(mpr - kLift - mr);  // weights of the product to those of the sum, but for 2^-ve
-#pragma unroll
           for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
             tmem_ld32x32b_x32(sc + 32 * c, x);
+            const float2 ks = *reinterpret_cast<const float2*>(&me.ks[2 * c]), ve = *reinterpret_cast<const float2*>(&me.ve[2 * c]),
+                         iv = *reinterpret_cast<const float2*>(&me.iv[2 * c]);
+            // never 0: a hidden score, -inf, times it stays -inf
+            const float cb[2] = {fmaxf(unit * ks.x, 1e-37f), fmaxf(unit * ks.y, 1e-37f)};
             tmem_wait_ld();
+            if (!whole) {
+              const uint32_t see = seen(c);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(see >> j & 1)) x[j] = 0xFF800000u;
+            }
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              t0 = fmaxf(t0, __uint_as_float(x[j]));
+              t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
+            }
+            t0 *= cb[0];
+            t1 *= cb[1];
+            const float top = fmaxf(t0, t1), topv = fmaxf(t0 + ve.x, t1 + ve.y);
+            const bool up = topv > mp + kSlack, up_sum = top > m + kSlack;
+            if (__any_sync(~0u, up || up_sum)) {
+              if (up_sum) {
+                l *= m == -INFINITY ? 1.f : ex2(m - top);
+                m = top;
+              }
+              const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
+              if (up) mp = topv;
+              mpr = mp == -INFINITY ? 0.f : mp;
+              back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));
+              if (__any_sync(~0u, f != 1.f)) {
+                uint32_t y[16];
+                if (k >= 2) {
+#pragma unroll 1
+                  for (int q = 0; q < D / 16; ++q) {
+                    tmem_ld32x32b_x16(oc + 16 * q, y);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                    tmem_st32x32b_x16(oc + 16 * q, y);
+                  }
+                }
+                tmem_wait_st();
+                const __half2 fh = __float2half2_rn(f);
+#pragma unroll 1
+                for (int q = 0; q < c; ++q) {
+                  tmem_ld32x32b_x16(sc + 16 * q, y);
+                  tmem_wait_ld();
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) {
+                    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[j]), fh);
+                    y[j] = *reinterpret_cast<const uint32_t*>(&h);
+                  }
+                  tmem_st32x32b_x16(sc + 16 * q, y);
+                }
+                tmem_wait_st();
+              }
+            }
             uint32_t y[16];
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-              const float cb = unit * me.ks[2 * c + u], off = me.ve[2 * c + u] - mpr + kLift;
-              float sum = 0.f;
+              const float off = (u ? ve.y : ve.x) - mpr + kLift;
+              float sum[2] = {0.f, 0.f};
 #pragma unroll
               for (int j = 0; j < 16; j += 2) {
-                float e0, e1;
-                if (whole) {
-                  e0 = ex2(fmaf(__uint_as_float(x[16 * u + j]), cb, off));
-                  e1 = ex2(fmaf(__uint_as_float(x[16 * u + j + 1]), cb, off));
-                } else {
-                  e0 = hidden(32 * c + 16 * u + j) ? 0.f : ex2(fmaf(__uint_as_float(x[16 * u + j]), cb, off));
-                  e1 = hidden(32 * c + 16 * u + j + 1) ? 0.f : ex2(fmaf(__uint_as_float(x[16 * u + j + 1]), cb, off));
+                float e[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                  const float d = fmaf(__uint_as_float(x[16 * u + j + q]), cb[u], off);
+                  // one exponential in four by FMAs: the other three keep the special-function unit busy
+                  e[q] = (j + q) % 4 == 3 ? ex2_fma(d) : ex2(d);
+                  sum[q] += e[q];
                 }
-                sum += e0 + e1;
-                y[8 * u + j / 2] = pack_f16(e0, e1);
+                y[8 * u + j / 2] = pack_f16(e[0], e[1]);
               }
-              l += sum == 0.f ? 0.f : sum * (back * me.iv[2 * c + u]);
+              l = fmaf(sum[0] + sum[1], back * (u ? iv.y : iv.x), l);
             }
             tmem_st32x32b_x16(sc + 16 * c, y);
           }
@@ -599,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&T.pf[s]);
       }
+      if (m == -INFINITY && l == l) l = 0.f;  // a row that saw nothing (ex2_fma's least weights aside)
       // both halves together: each warpgroup takes half of the dims
       ok = __all_sync(~0u, ok && wait(&T.of, items & 1));
       tc_fence_after();
