@@ -13,6 +13,8 @@
 //
 // What bounds it: the exponentials (16 a clock and SM: 1024 clocks a tile) and the products (1024 clocks) for full
 // items; with half the rows or fewer the cache's bytes.
+#include <type_traits>
+
 #include "kv.cuh"
 
 namespace pivot {
@@ -24,7 +26,7 @@ constexpr int kTileB = kTok * D;             // bytes of an e4m3 tile
 constexpr int kSoft = 256, kConv = 128;      // threads: two softmax warpgroups, one of the converters
 constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWMma = kWTma + 1;
 constexpr int kThreads = 32 * (kWMma + 1);
-constexpr float kLift = 7.f, kSlack = 8.f;   // weights up to 2^(7+8): the maxima may lag by 2^8 before sums are rescaled
+constexpr float kLift = 2.f, kSlack = 13.f;  // weights up to 2^15: the maxima may lag by 2^13 before sums are rescaled
 
 struct Meta {  // of a tile's 8 blocks
   float ks[8], ve[8], iv[8];  // 2^ke, ve, 2^-ve
@@ -229,17 +231,24 @@ constexpr int kOffQ = 0, kOffK = 2 * M * D, kOffV = kOffK + kKS * kTileB, kOffH 
 constexpr size_t kSmem = kOffTail + sizeof(Tail);
 static_assert(kSmem <= 232448, "227 KB of dynamic shared memory per CTA");
 
-// 2^x without the special-function unit, for x < 127: 2^r of r = x - round(x) in [-1/2, 1/2] by a polynomial that
-// interpolates it at the five Chebyshev points (relative error below 4e-6), times 2^round(x).
-__device__ __forceinline__ float ex2_fma(float x) {
-  const float c = x < -126.f ? -126.f : x;
-  const float t = c + 12582912.f;  // 1.5 * 2^23: the low bits hold round(c)
-  const float r = c - (t - 12582912.f);
-  float p = fmaf(0.00966636837f, r, 0.0559219755f);
-  p = fmaf(p, r, 0.240223497f);
-  p = fmaf(p, r, 0.693121016f);
-  p = fmaf(p, r, 1.f);
-  return p * __int_as_float((__float_as_int(t) << 23) + 0x3F800000);  // a product, so that NaN stays NaN
+// Two fp32 values in one register pair, for the packed instructions.
+__device__ __forceinline__ uint64_t two(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 
 // Whether every row of the item sees every token of a tile (where its pages are present).
@@ -558,100 +567,103 @@ __global__ void __launch_bounds__(kThreads, 1)
             return below(upto - 32 * c) & (~below(from - 32 * c) | below(sinks - 32 * c)) & there;
           };
           // One pass over S, 32 columns at a time.  The weights' reference m' (and m, the sum's) may lag behind the
-          // largest score by 2^8; where it would by more, what was weighed with the old one is scaled down: the
+          // largest score by 2^13; where it would by more, what was weighed with the old one is scaled down: the
           // output sums, and this tile's weights so far.  After the first columns of an item that is rare.
           // The loop is not unrolled: its code then stays in the instruction cache (unrolled it ran at half the speed).
           float mpr = mp == -INFINITY ? 0.f : mp;
           float back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));  // product's weights to the sum's, but for 2^-ve
+          auto weigh = [&](auto all) {  // two copies: as one, the compiler masks every tile
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
-            tmem_ld32x32b_x32(sc + 32 * c, x);
-            const float2 ks = *reinterpret_cast<const float2*>(&me.ks[2 * c]), ve = *reinterpret_cast<const float2*>(&me.ve[2 * c]),
-                         iv = *reinterpret_cast<const float2*>(&me.iv[2 * c]);
-            // never 0: a hidden score, -inf, times it stays -inf
-            const float cb[2] = {fmaxf(unit * ks.x, 1e-37f), fmaxf(unit * ks.y, 1e-37f)};
-            tmem_wait_ld();
-            if (!whole) {
-              const uint32_t see = seen(c);
+            for (int c = 0; c < 4; ++c) {
+              uint32_t x[32];
+              tmem_ld32x32b_x32(sc + 32 * c, x);
+              const float2 ks = *reinterpret_cast<const float2*>(&me.ks[2 * c]), ve = *reinterpret_cast<const float2*>(&me.ve[2 * c]),
+                           iv = *reinterpret_cast<const float2*>(&me.iv[2 * c]);
+              // never 0: a hidden score, -inf, times it stays -inf
+              const float cb[2] = {fmaxf(unit * ks.x, 1e-37f), fmaxf(unit * ks.y, 1e-37f)};
+              tmem_wait_ld();
+              if (!all) {
+                const uint32_t see = seen(c);
 #pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(see >> j & 1)) x[j] = 0xFF800000u;
-            }
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              t0 = fmaxf(t0, __uint_as_float(x[j]));
-              t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
-            }
-            t0 *= cb[0];
-            t1 *= cb[1];
-            const float top = fmaxf(t0, t1), topv = fmaxf(t0 + ve.x, t1 + ve.y);
-            const bool up = topv > mp + kSlack, up_sum = top > m + kSlack;
-            if (__any_sync(~0u, up || up_sum)) {
-              if (up_sum) {
-                l *= m == -INFINITY ? 1.f : ex2(m - top);
-                m = top;
+                for (int j = 0; j < 32; ++j)
+                  if (!(see >> j & 1)) x[j] = 0xFF800000u;
               }
-              const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
-              if (up) mp = topv;
-              mpr = mp == -INFINITY ? 0.f : mp;
-              back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));
-              if (__any_sync(~0u, f != 1.f)) {
-                uint32_t y[16];
-                if (k >= 2) {
+              float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                t0 = fmaxf(t0, __uint_as_float(x[j]));
+                t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
+              }
+              t0 *= cb[0];
+              t1 *= cb[1];
+              const float top = fmaxf(t0, t1), topv = fmaxf(t0 + ve.x, t1 + ve.y);
+              const bool up = topv > mp + kSlack, up_sum = top > m + kSlack;
+              if (__any_sync(~0u, up || up_sum)) {
+                if (up_sum) {
+                  l *= m == -INFINITY ? 1.f : ex2(m - top);
+                  m = top;
+                }
+                const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
+                if (up) mp = topv;
+                mpr = mp == -INFINITY ? 0.f : mp;
+                back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));
+                if (__any_sync(~0u, f != 1.f)) {
+                  uint32_t y[16];
+                  if (k >= 2) {
 #pragma unroll 1
-                  for (int q = 0; q < D / 16; ++q) {
-                    tmem_ld32x32b_x16(oc + 16 * q, y);
+                    for (int q = 0; q < D / 16; ++q) {
+                      tmem_ld32x32b_x16(oc + 16 * q, y);
+                      tmem_wait_ld();
+#pragma unroll
+                      for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+                      tmem_st32x32b_x16(oc + 16 * q, y);
+                    }
+                  }
+                  tmem_wait_st();
+                  const __half2 fh = __float2half2_rn(f);
+#pragma unroll 1
+                  for (int q = 0; q < c; ++q) {
+                    tmem_ld32x32b_x16(sc + 16 * q, y);
                     tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                    tmem_st32x32b_x16(oc + 16 * q, y);
+                    for (int j = 0; j < 16; ++j) {
+                      const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[j]), fh);
+                      y[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    tmem_st32x32b_x16(sc + 16 * q, y);
                   }
+                  tmem_wait_st();
                 }
-                tmem_wait_st();
-                const __half2 fh = __float2half2_rn(f);
-#pragma unroll 1
-                for (int q = 0; q < c; ++q) {
-                  tmem_ld32x32b_x16(sc + 16 * q, y);
-                  tmem_wait_ld();
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) {
-                    const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[j]), fh);
-                    y[j] = *reinterpret_cast<const uint32_t*>(&h);
-                  }
-                  tmem_st32x32b_x16(sc + 16 * q, y);
-                }
-                tmem_wait_st();
               }
-            }
-            uint32_t y[16];
+              uint32_t y[16];
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float off = (u ? ve.y : ve.x) - mpr + kLift;
-              float sum[2] = {0.f, 0.f};
+              for (int u = 0; u < 2; ++u) {
+                const float off = (u ? ve.y : ve.x) - mpr + kLift;
+                const uint64_t off2 = two(off, off), cb2 = two(cb[u], cb[u]);
+                uint64_t sum = two(0.f, 0.f);
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float e[2];
-#pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  const float d = fmaf(__uint_as_float(x[16 * u + j + q]), cb[u], off);
-                  // one exponential in four by FMAs: the other three keep the special-function unit busy
-                  e[q] = (j + q) % 4 == 3 ? ex2_fma(d) : ex2(d);
-                  sum[q] += e[q];
+                for (int j = 0; j < 16; j += 2) {
+                  float d0, d1;
+                  split(fma2(two(__uint_as_float(x[16 * u + j]), __uint_as_float(x[16 * u + j + 1])), cb2, off2), d0, d1);
+                  d0 = ex2(d0);
+                  d1 = ex2(d1);
+                  sum = add2(sum, two(d0, d1));
+                  y[8 * u + j / 2] = pack_f16(d0, d1);
                 }
-                y[8 * u + j / 2] = pack_f16(e[0], e[1]);
+                float s0, s1;
+                split(sum, s0, s1);
+                l = fmaf(s0 + s1, back * (u ? iv.y : iv.x), l);
               }
-              l = fmaf(sum[0] + sum[1], back * (u ? iv.y : iv.x), l);
+              tmem_st32x32b_x16(sc + 16 * c, y);
             }
-            tmem_st32x32b_x16(sc + 16 * c, y);
-          }
+          };
+          if (whole) weigh(std::true_type{});
+          else weigh(std::false_type{});
           tmem_wait_st();
         }
         tc_fence_before();
         mbar_arrive(&T.pf[s]);
       }
-      if (m == -INFINITY && l == l) l = 0.f;  // a row that saw nothing (ex2_fma's least weights aside)
       // both halves together: each warpgroup takes half of the dims
       ok = __all_sync(~0u, ok && wait(&T.of, items & 1));
       tc_fence_after();
