@@ -614,6 +614,7 @@ class KVCache:
         self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
         self.device, self.num_pages, self.kv_heads, self.page_size, self.d = k.device, pages, heads, page, d
         self._c = _CacheC(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, heads, page, d)
+        self._ref = ctypes.byref(self._c)
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, d: int, device="cuda") -> "KVCache":
@@ -624,64 +625,52 @@ class KVCache:
                    *(torch.zeros(exps, dtype=torch.int8, device=device) for _ in range(2)))
 
 
-class _On:
-    """The call's device made current, and its stream (the device's current one unless given)."""
+# torch.cuda.current_stream builds a Stream object (3 us); these calls need its handle alone
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda i: torch.cuda.current_stream(i).cuda_stream)
 
-    def __init__(self, device, stream):
-        self.guard = None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
-        self.stream, self.device = stream, device
 
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-        if self.stream is None:
-            self.stream = torch.cuda.current_stream(self.device)
-        elif self.stream.device != self.device:
-            self.__exit__(None, None, None)
-            raise ValueError(f"the stream is of {self.stream.device}, the cache is on {self.device}")
-        return self
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-    def new(self, shape, dtype):
-        """A tensor that belongs to the call's stream."""
-        if self.stream == torch.cuda.current_stream(self.device):
-            return torch.empty(shape, dtype=dtype, device=self.device)
-        with torch.cuda.stream(self.stream):
-            return torch.empty(shape, dtype=dtype, device=self.device)
+def _kv_elsewhere(cache, stream):
+    """The stream to make current for the call (with its device), or None where the current one is right."""
+    if stream is None:
+        return None if torch.cuda.current_device() == cache.device.index else torch.cuda.current_stream(cache.device)
+    if stream.device != cache.device:
+        raise ValueError(f"the stream is of {stream.device}, the cache is on {cache.device}")
+    return stream
 
 
 def _kv_rows(name, t, heads, cache, dtype=None):
-    """Checks a row tensor [rows, heads, d] whose rows may be slices of a wider one."""
-    if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.shape[2] != cache.d or (heads and t.shape[1] != heads):
+    """Checks a row tensor [rows, heads, d] whose rows may be slices of a wider one; returns its row stride."""
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.d or (heads and shape[1] != heads):
         raise ValueError(f"{name} must be [rows, {heads or 'heads'}, {cache.d}]")
-    _dt(t)
-    if t.device != cache.device or (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name} must be on {cache.device}, of the same type as the other rows")
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != cache.d):
+    if t.dtype is not dtype and (dtype is not None or t.dtype not in _KV_TYPES):
+        raise TypeError(f"{name} must be bfloat16 or float32, of the same type as the other rows, got {t.dtype}")
+    if t.device != cache.device:
+        raise ValueError(f"{name} must be on {cache.device}")
+    r, h, e = t.stride()
+    if e != 1 or (h != cache.d and shape[1] > 1):
         raise ValueError(f"{name}: each row's heads must be contiguous")
+    return r if shape[0] > 1 else max(r, shape[1] * shape[2])
 
 
-def _row_stride(t):
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+_KV_TYPES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
-def _kv_step(cache, block_table, row_offsets, lens, rows, stream):
+def _kv_step(cache, block_table, row_offsets, lens, rows):
     """The step's C struct, and what it points to."""
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.device != cache.device or \
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32 or block_table.device != cache.device or \
             block_table.shape[1] == 0 or block_table.stride(1) != 1:
         raise ValueError(f"block_table must be an int32 [B, width] tensor on {cache.device}, its rows contiguous")
     B, width = block_table.shape
-    off = _positions_dev(row_offsets, cache.device, stream)
-    n = _positions_dev(lens, cache.device, stream)
-    for t, m, name in ((off, B + 1, "row_offsets"), (n, B, "lens")):
-        if t.dtype != torch.int64 or t.shape != (m,) or not t.is_contiguous():
-            raise ValueError(f"{name} must be {m} contiguous int64 values")
-    step = _StepC(block_table.data_ptr(), off.data_ptr(), n.data_ptr(),
-                  block_table.stride(0) if B > 1 else max(block_table.stride(0), width), rows, width, B)
-    return step, (off, n)
+    off = _positions_dev(row_offsets, cache.device, None)
+    n = _positions_dev(lens, cache.device, None)
+    if off.dtype is not torch.int64 or off.shape != (B + 1,) or not off.is_contiguous():
+        raise ValueError(f"row_offsets must be {B + 1} contiguous int64 values")
+    if n.dtype is not torch.int64 or n.shape != (B,) or not n.is_contiguous():
+        raise ValueError(f"lens must be {B} contiguous int64 values")
+    stride = block_table.stride(0) if B > 1 else max(block_table.stride(0), width)
+    return _StepC(block_table.data_ptr(), off.data_ptr(), n.data_ptr(), stride, rows, width, B), (off, n)
 
 
 def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None, sin=None, interleaved: bool = False,
@@ -695,8 +684,13 @@ def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None,
     rotate the first rot dims of k, and of q [rows, heads, d] into q_out (a new tensor unless given; q
     itself is allowed): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no
     token leave cache and q_out as they were."""
-    _kv_rows("k", k, cache.kv_heads, cache)
-    _kv_rows("v", v, cache.kv_heads, cache, k.dtype)
+    other = _kv_elsewhere(cache, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return kv_append(cache, k, v, block_table, row_offsets, lens, cos=cos, sin=sin, interleaved=interleaved,
+                             q=q, q_out=q_out)
+    ks = _kv_rows("k", k, cache.kv_heads, cache)
+    vs = _kv_rows("v", v, cache.kv_heads, cache, k.dtype)
     rows = k.shape[0]
     if v.shape[0] != rows:
         raise ValueError("k and v must have the same rows")
@@ -704,61 +698,66 @@ def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None,
     if (cos is None) != (sin is None):
         raise ValueError("cos and sin go together")
     if cos is not None:
-        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype != torch.float32 or sin.dtype != torch.float32 or \
-                cos.device != cache.device or sin.device != cache.device or not cos.is_contiguous() or \
-                not sin.is_contiguous():
+        if cos.dim() != 2 or cos.shape != sin.shape or cos.dtype is not torch.float32 or \
+                sin.dtype is not torch.float32 or cos.device != cache.device or sin.device != cache.device or \
+                not cos.is_contiguous() or not sin.is_contiguous():
             raise ValueError(f"cos and sin must be contiguous fp32 [positions, rot / 2] tensors on {cache.device}")
         n_pos, rot = cos.shape[0], 2 * cos.shape[1]
+    heads = qs = qos = 0
     if q is not None:
-        _kv_rows("q", q, 0, cache, k.dtype)
+        qs = _kv_rows("q", q, 0, cache, k.dtype)
+        heads = q.shape[1]
         if q.shape[0] != rows:
             raise ValueError("q must have k's rows")
-        if q_out is not None:
-            _kv_rows("q_out", q_out, q.shape[1], cache, k.dtype)
-            if q_out.shape[0] != rows:
-                raise ValueError("q_out must have q's rows")
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+        qos = _kv_rows("q_out", q_out, heads, cache, k.dtype)
+        if q_out.shape[0] != rows:
+            raise ValueError("q_out must have q's rows")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    with _On(cache.device, stream) as on:
-        step, _keep = _kv_step(cache, block_table, row_offsets, lens, rows, on.stream)
-        if rows == 0:
-            return q_out if q_out is not None or q is None else q.new_empty(q.shape)
-        if q is not None and q_out is None:
-            q_out = on.new(q.shape, q.dtype)
+    step, _keep = _kv_step(cache, block_table, row_offsets, lens, rows)
+    if rows:
         _check(lib().pivot_kv_append(
-            ctypes.byref(cache._c), ctypes.byref(step), k.data_ptr(), _row_stride(k), v.data_ptr(), _row_stride(v),
-            _dt(k), _ptr(cos), _ptr(sin), n_pos, rot, int(interleaved), _ptr(q), 0 if q is None else _row_stride(q),
-            0 if q is None else q.shape[1], _ptr(q_out), 0 if q is None else _row_stride(q_out),
-            on.stream.cuda_stream), "pivot_kv_append")
+            cache._ref, ctypes.byref(step), k.data_ptr(), ks, v.data_ptr(), vs, _KV_TYPES[k.dtype],
+            None if cos is None else cos.data_ptr(), None if sin is None else sin.data_ptr(), n_pos, rot,
+            int(interleaved), None if q is None else q.data_ptr(), qs, heads,
+            None if q is None else q_out.data_ptr(), qos, _raw_stream(cache.device.index)), "pivot_kv_append")
     return q_out
 
 
-def _kv_attention(where, q, cache, block_table, row_offsets, lens, scale, lse, out, ws, stream, topk, call):
-    _kv_rows("q", q, 0, cache)
-    rows, heads, d = q.shape
-    if out is not None and (out.shape != q.shape or out.dtype != q.dtype or out.device != q.device or
-                            not out.is_contiguous()):
-        raise ValueError("out must be a contiguous tensor of q's shape, type and device")
-    given = isinstance(lse, torch.Tensor)
-    if given and (lse.shape != (rows, heads) or lse.dtype != torch.float32 or lse.device != q.device or
-                  not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous fp32 [rows, heads] tensor on q's device")
-    with _On(cache.device, stream) as on:
-        step, _keep = _kv_step(cache, block_table, row_offsets, lens, rows, on.stream)
-        if out is None:
-            out = on.new((rows, heads, d), q.dtype)
-        z = lse if given else on.new((rows, heads), torch.float32) if lse else None
-        if rows == 0:
-            return out, z
-        nbytes = int(lib().pivot_kv_workspace_size(rows, step.B, heads, cache.kv_heads, d, topk, _dt(q)))
-        if nbytes == 0:
+_kv_sizes: dict = {}
+
+
+def _kv_scratch(rows, B, heads, cache, topk, dt, ws, where):
+    """The call's workspace: scratch of this call alone unless the caller keeps one, so that calls on two streams,
+    and captured ones, share none."""
+    key = (cache.device.index, rows, B, heads, cache.kv_heads, cache.d, topk, dt)
+    n = _kv_sizes.get(key)
+    if n is None:
+        n = int(lib().pivot_kv_workspace_size(rows, B, heads, cache.kv_heads, cache.d, topk, dt))
+        if n == 0:
             raise PivotError(2, where, "unsupported shape")
-        # scratch of this call alone unless the caller keeps one: calls on two streams, and captured ones, share none
-        w = on.new((nbytes,), torch.uint8) if ws is None else ws.get(nbytes)
-        _check(call(ctypes.byref(cache._c), ctypes.byref(step), q.data_ptr(), _row_stride(q), heads, _dt(q),
-                    d ** -0.5 if scale is None else scale, out.data_ptr(), _ptr(z), w.data_ptr(), w.numel(),
-                    on.stream.cuda_stream), where)
-    return out, z
+        if len(_kv_sizes) > 4096:
+            _kv_sizes.clear()
+        _kv_sizes[key] = n
+    return torch.empty(n, dtype=torch.uint8, device=cache.device) if ws is None else ws.get(n)
+
+
+def _kv_results(q, cache, out, lse):
+    """out and lse as given, checked, or new."""
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    elif out.shape != q.shape or out.dtype is not q.dtype or out.device != q.device or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape, type and device")
+    if lse is True:
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
+    elif lse is False:
+        lse = None
+    elif lse is not None and (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or
+                              lse.device != q.device or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous fp32 [rows, heads] tensor on q's device")
+    return out, lse
 
 
 def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Optional[float] = None, window: int = 0,
@@ -771,11 +770,23 @@ def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Op
     that receives ln sum exp(scale q.k).  Rows that see nothing give zeros and -inf; rows behind
     row_offsets[B] are not written (they are undefined in an ``out`` that the call allocates)."""
 
-    def call(c, s, qp, qs, h, dt, sc, o, z, w, wb, st):
-        return lib().pivot_kv_attention(c, s, qp, qs, h, dt, sc, window, sinks, o, z, w, wb, st)
-
-    return _kv_attention("pivot_kv_attention", q, cache, block_table, row_offsets, lens, scale, lse, out, ws, stream,
-                         0, call)
+    other = _kv_elsewhere(cache, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return kv_attention(q, cache, block_table, row_offsets, lens, scale=scale, window=window, sinks=sinks,
+                                lse=lse, out=out, ws=ws)
+    qs = _kv_rows("q", q, 0, cache)
+    rows, heads, d = q.shape
+    dt = _KV_TYPES[q.dtype]
+    step, _keep = _kv_step(cache, block_table, row_offsets, lens, rows)
+    out, lse = _kv_results(q, cache, out, lse)
+    if rows:
+        w = _kv_scratch(rows, step.B, heads, cache, 0, dt, ws, "pivot_kv_attention")
+        _check(lib().pivot_kv_attention(
+            cache._ref, ctypes.byref(step), q.data_ptr(), qs, heads, dt, d ** -0.5 if scale is None else scale, window,
+            sinks, out.data_ptr(), None if lse is None else lse.data_ptr(), w.data_ptr(), w.numel(),
+            _raw_stream(cache.device.index)), "pivot_kv_attention")
+    return out, lse
 
 
 def kv_attention_selected(q, cache: KVCache, indices, block_table, row_offsets, lens, *,
@@ -786,18 +797,28 @@ def kv_attention_selected(q, cache: KVCache, indices, block_table, row_offsets, 
     indices int32 [rows, k]: the indexer's rows (reuse, refine, indexer_dense and their batch forms), or any
     list of positions of the row's sequence; entries below 0 or behind the row's own position count as
     absent, an entry listed twice counts twice.  The rest as kv_attention."""
-    if indices.dim() != 2 or indices.dtype != torch.int32 or indices.shape[0] != q.shape[0] or \
+    other = _kv_elsewhere(cache, stream)
+    if other is not None:
+        with torch.cuda.stream(other):
+            return kv_attention_selected(q, cache, indices, block_table, row_offsets, lens, scale=scale, lse=lse,
+                                         out=out, ws=ws)
+    qs = _kv_rows("q", q, 0, cache)
+    rows, heads, d = q.shape
+    if indices.dim() != 2 or indices.dtype is not torch.int32 or indices.shape[0] != rows or \
             indices.shape[1] == 0 or indices.device != cache.device or indices.stride(1) != 1:
         raise ValueError(f"indices must be an int32 [rows, k] tensor on {cache.device}, its rows contiguous")
     topk = indices.shape[1]
-    stride = indices.stride(0) if indices.shape[0] > 1 else max(indices.stride(0), topk)
-
-    def call(c, s, qp, qs, h, dt, sc, o, z, w, wb, st):
-        return lib().pivot_kv_attention_selected(c, s, qp, qs, h, dt, sc, indices.data_ptr(), stride, topk, o, z, w,
-                                                 wb, st)
-
-    return _kv_attention("pivot_kv_attention_selected", q, cache, block_table, row_offsets, lens, scale, lse, out, ws,
-                         stream, topk, call)
+    dt = _KV_TYPES[q.dtype]
+    step, _keep = _kv_step(cache, block_table, row_offsets, lens, rows)
+    out, lse = _kv_results(q, cache, out, lse)
+    if rows:
+        w = _kv_scratch(rows, step.B, heads, cache, topk, dt, ws, "pivot_kv_attention_selected")
+        _check(lib().pivot_kv_attention_selected(
+            cache._ref, ctypes.byref(step), q.data_ptr(), qs, heads, dt, d ** -0.5 if scale is None else scale,
+            indices.data_ptr(), indices.stride(0) if rows > 1 else max(indices.stride(0), topk), topk, out.data_ptr(),
+            None if lse is None else lse.data_ptr(), w.data_ptr(), w.numel(), _raw_stream(cache.device.index)),
+            "pivot_kv_attention_selected")
+    return out, lse
 
 
 def last_device_status(ws: Workspace, stream=None) -> int:

@@ -6,6 +6,7 @@
 #include <cuda_fp8.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "kernels.cuh"
 #include "ptx.cuh"
@@ -74,6 +75,20 @@ struct KvLine {
 
 // Partial result of an item of `rows` query rows: sums [rows][d], then (m', m, l, 0) of each row.
 __host__ __device__ constexpr size_t kv_part_floats(int rows, int d) { return (size_t)rows * (d + 4); }
+
+// Lets a kernel use its dynamic shared memory, once on each device.
+template <auto kKernel>
+cudaError_t kv_allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (dev < 64 && (done.load(std::memory_order_relaxed) & bit)) return cudaSuccess;
+  e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess && dev < 64) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
 
 size_t kv_attn_workspace(int sms, int d);
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, const int* gate, cudaStream_t s);

@@ -731,8 +731,7 @@ KvLine carve_line(void* ws, int ctas) {
 template <int D, bool BF16, bool SEL>
 cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaStream_t s) {
   using Sh = Shape<D, BF16, SEL>;
-  cudaError_t e = cudaFuncSetAttribute(kv_attn_kernel<D, BF16, SEL>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       (int)Sh::kBytes);
+  cudaError_t e = kv_allow_smem<kv_attn_kernel<D, BF16, SEL>>(Sh::kBytes);
   if (e != cudaSuccess) return e;
   kv_attn_kernel<D, BF16, SEL><<<ctas, kThreads, Sh::kBytes, s>>>(a, line);
   e = cudaGetLastError();

@@ -757,7 +757,7 @@ cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, cons
   t.line.part = reinterpret_cast<float*>(p + 256 + (size_t)sms * sizeof(KvOpen));
   t.slots = (int64_t)a.c.pages * a.c.hk * a.c.ps;
   t.timeout_ns = timeout_ns;
-  e = cudaFuncSetAttribute(kv_attn_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+  e = kv_allow_smem<kv_attn_tc_kernel>(kSmem);
   if (e != cudaSuccess) return e;
   kv_attn_tc_kernel<<<sms, kThreads, kSmem, s>>>(kmap, vmap, t);
   e = cudaGetLastError();
