@@ -315,7 +315,7 @@ PIVOT_API pivot_status pivot_decode_rowselect(const uint32_t *keys, const int32_
  *
  * The cache holds a key as k = payload * 2^e: payload an OCP e4m3 byte, e one int8 exponent for each block of
  * PIVOT_KV_BLOCK tokens and head; values likewise.  k, v [num_pages, kv_heads, page_size, d] bytes; k_exp, v_exp
- * [num_pages, kv_heads, page_size / PIVOT_KV_BLOCK].  kv_heads >= 1; page_size a positive multiple of
+ * [num_pages, kv_heads, page_size / PIVOT_KV_BLOCK].  kv_heads 1 .. 1024; page_size a positive multiple of
  * PIVOT_KV_BLOCK; d = 64 or 128; k and v 16-byte aligned; num_pages * kv_heads * page_size < 2^31.  An exponent
  * outside [-60, 60] is never written; what reads one outside that range gives is undefined (and faults nothing).
  *

@@ -59,7 +59,7 @@ def select(lib, c, s, **kw):
 
 BAD_CACHE = [(dict(k=None), 1), (dict(v_exp=None), 1), (dict(k=PTR + 8), 1), (dict(num_pages=0), 1),
              (dict(kv_heads=0), 1), (dict(page_size=0), 1), (dict(page_size=24), 1), (dict(page_size=-16), 1),
-             (dict(d=96), 2), (dict(d=0), 2), (dict(num_pages=1 << 25, page_size=64), 2)]
+             (dict(d=96), 2), (dict(d=0), 2), (dict(kv_heads=1025), 2), (dict(num_pages=1 << 25, page_size=64), 2)]
 BAD_STEP = [(dict(block_table=None), 1), (dict(row_offsets=None), 1), (dict(lens=None), 1), (dict(B=0), 1),
             (dict(rows=-1), 1), (dict(table_width=0), 1), (dict(table_stride=3), 1), (dict(rows=2 ** 31 - 1), 2),
             (dict(table_width=1 << 26, table_stride=1 << 26), 2)]

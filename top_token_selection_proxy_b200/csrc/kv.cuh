@@ -37,7 +37,7 @@ struct KvAppendArgs {
   int64_t k_stride, v_stride, q_stride, q_out_stride;  // elements
   const float *cos, *sin;  // [n_pos, rot / 2]
   int64_t n_pos;
-  int rot, interleaved, hq, rows_per_cta;
+  int rot, interleaved, hq, rows_per_cta, kv_slices;
   bool is_bf16;
 };
 

@@ -9,12 +9,13 @@
 // What bounds it: bytes (a key row is read once at 2 or 4 bytes an element and written at 1, a query row is read
 // and written).  A block is one warp's work for one head and one of k and v: its (up to 16) token rows stay in
 // registers between the maximum and the rounding, so nothing is read twice; 8 elements a lane, 16-byte loads.
+// Query rows are other CTAs' work: a warp keeps a row's angles and takes its heads in batches of loads.
 #include "kv.cuh"
 
 namespace pivot {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kE = 8;  // elements a lane holds of a row
 
 template <bool BF16>
@@ -82,37 +83,66 @@ __device__ __forceinline__ Turn turn_of(int rot, int interleaved, int lane) {
   return t;
 }
 
-// x turned by the angles of one position, in T's arithmetic (float, or double where an exponent is in doubt).
-// All lanes of the warp take part; `live` lanes have a row.
-template <typename T>
-__device__ __forceinline__ void rotate(const float (&x)[kE], T (&y)[kE], const Turn& t, bool live, const float* cos,
-                                       const float* sin, int64_t pos, int half) {
+// The angles that a lane's 8 elements take at one position.
+struct Angles {
   float c[kE], s[kE];
-  const bool go = live && t.on;
+};
+
+__device__ __forceinline__ Angles angles_at(const Turn& t, bool go, const float* cos, const float* sin, int64_t pos,
+                                            int half) {
+  Angles a;
+#pragma unroll
+  for (int i = 0; i < kE; ++i) a.c[i] = 1.f, a.s[i] = 0.f;
   if (go) {
     const float4* pc = reinterpret_cast<const float4*>(cos + pos * half + t.entry);
     const float4* ps = reinterpret_cast<const float4*>(sin + pos * half + t.entry);
     const float4 c0 = __ldg(pc), s0 = __ldg(ps);
-    c[0] = c0.x, c[1] = c0.y, c[2] = c0.z, c[3] = c0.w;
-    s[0] = s0.x, s[1] = s0.y, s[2] = s0.z, s[3] = s0.w;
+    a.c[0] = c0.x, a.c[1] = c0.y, a.c[2] = c0.z, a.c[3] = c0.w;
+    a.s[0] = s0.x, a.s[1] = s0.y, a.s[2] = s0.z, a.s[3] = s0.w;
     if (t.split) {
       const float4 c1 = __ldg(pc + 1), s1 = __ldg(ps + 1);
-      c[4] = c1.x, c[5] = c1.y, c[6] = c1.z, c[7] = c1.w;
-      s[4] = s1.x, s[5] = s1.y, s[6] = s1.z, s[7] = s1.w;
+      a.c[4] = c1.x, a.c[5] = c1.y, a.c[6] = c1.z, a.c[7] = c1.w;
+      a.s[4] = s1.x, a.s[5] = s1.y, a.s[6] = s1.z, a.s[7] = s1.w;
     }
   }
+  return a;
+}
+
+// a c + b s in fp32.
+__device__ __forceinline__ float turned(float a, float c, float b, float s) { return fmaf(b, s, a * c); }
+
+// a c + b s rounded to odd at 24 bits: the exact value's neighbour whose last bit is set, unless it is exact.  A
+// later rounding to fewer bits, and a comparison with a power of two times 448, then give what the exact value
+// gives.  The products' and the sum's own errors are exact fp32 values (fused multiply-add; Knuth's two-sum).
+__device__ __forceinline__ float turned_odd(float a, float c, float b, float s) {
+  const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
+  const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
+  const float sum = __fadd_rn(p, q), v = __fsub_rn(sum, p);
+  const float es = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, v)), __fsub_rn(q, v));
+  const float low = __fadd_rn(es, __fadd_rn(ep, eq));
+  const float hi = __fadd_rn(sum, low);
+  const float rest = __fsub_rn(low, __fsub_rn(hi, sum));
+  const int bits = __float_as_int(hi);
+  if ((rest > 0.f || rest < 0.f) && !(bits & 1)) return __int_as_float((rest > 0.f) == (hi > 0.f) ? bits + 1 : bits - 1);
+  return hi;  // exact, odd already, or not finite
+}
+
+// x turned: F(a, c, b, s) forms each element.  All lanes of the warp take part.
+template <typename F>
+__device__ __forceinline__ void rotate(float (&x)[kE], const Turn& t, const Angles& a, F form) {
   if (t.split) {
+    const float sign = t.on ? t.sign : 0.f;
 #pragma unroll
     for (int i = 0; i < kE; ++i) {
       const float other = __shfl_sync(~0u, x[i], t.peer);
-      y[i] = go ? (T)x[i] * (T)c[i] + (T)(t.sign * other) * (T)s[i] : (T)x[i];
+      x[i] = t.on ? form(x[i], a.c[i], other, sign * a.s[i]) : x[i];
     }
-  } else {
+  } else if (t.on) {
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) {
-      const T a = x[2 * i], b = x[2 * i + 1];
-      y[2 * i] = go ? a * (T)c[i] - b * (T)s[i] : a;
-      y[2 * i + 1] = go ? b * (T)c[i] + a * (T)s[i] : b;
+      const float u = x[2 * i], w = x[2 * i + 1];
+      x[2 * i] = form(u, a.c[i], w, -a.s[i]);
+      x[2 * i + 1] = form(w, a.c[i], u, a.s[i]);
     }
   }
 }
@@ -160,48 +190,14 @@ __device__ void append_block(const KvAppendArgs& a, bool is_key, int head, int p
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const uint32_t p = base + i * kRows + slot;
-    const bool live = p >= p0 && p < p1;
-    if (rot) {
-      float x[kE];
-#pragma unroll
-      for (int j = 0; j < kE; ++j) x[j] = y[i][j];
-      rotate<float>(x, y[i], t, live, a.cos, a.sin, p, a.rot / 2);
-    }
+    if (rot)
+      rotate(y[i], t, angles_at(t, t.on && p >= p0 && p < p1, a.cos, a.sin, p, a.rot / 2), turned_odd);
 #pragma unroll
     for (int j = 0; j < kE; ++j) amax = fmaxf(amax, finite_abs(y[i][j]));
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
   int e = exponent_of(amax);
-  // A rotated maximum carries a rounding error of a few units; within 16 of a step between two exponents
-  // (1 block in 3 * 10^5) the step is decided in 64 bits.
-  const int near = (int)(__float_as_uint(amax) & 0x7FFFFFu) - 0x600000;
-  if (rot && near >= -16 && near <= 16) {
-    double m = 0.0;
-    for (int i = 0; i < kPasses; ++i) {
-      const uint32_t p = base + i * kRows + slot;
-      const bool live = p >= p0 && p < p1;
-      float x[kE];
-      double z[kE];
-#pragma unroll
-      for (int j = 0; j < kE; ++j) x[j] = 0.f;
-      if (live) load8<BF16>(src, (row0 + (p - p0)) * stride + head * D + sub * kE, x);
-      rotate<double>(x, z, t, live, a.cos, a.sin, p, a.rot / 2);
-#pragma unroll
-      for (int j = 0; j < kE; ++j) {
-        const double w = fabs(z[j]);
-        if (w <= 3.402823466e38 && w > m) m = w;
-      }
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      const double w = __shfl_xor_sync(~0u, m, o);
-      m = w > m ? w : m;
-    }
-    const int low = exponent_of(__uint_as_float((__float_as_uint(amax) & 0xFF800000u) | 0x600000u));  // at the step
-    e = low;
-    if (low < PIVOT_KV_EXP_MAX && m > 448.0 * (double)kv_exp2i(low)) e = low + 1;
-  }
   uint8_t* dst = is_key ? a.c.k : a.c.v;
   int8_t* exps = is_key ? a.c.ke : a.c.ve;
   const int64_t ph = (int64_t)page * a.c.hk + head;
@@ -243,54 +239,66 @@ __device__ void append_block(const KvAppendArgs& a, bool is_key, int head, int p
   if (lane == 0) *exp_at = (int8_t)e;
 }
 
-// A CTA takes `rows_per_cta` rows: the blocks whose first new token is among them (a block's other rows may
-// follow behind), and the rotation of their query rows.
+// A CTA takes `rows_per_cta` rows.  The first `kv_slices` of each such group append the blocks whose first new token
+// is among them (a block's other rows may follow behind), a warp for each of 8 of the heads of k and v; the others
+// rotate the query rows.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs a) {
-  constexpr int kLanes = D / kE, kRows = 32 / kLanes;
+__global__ void __launch_bounds__(kThreads, 2) kv_append_kernel(const KvAppendArgs a) {
+  constexpr int kLanes = D / kE, kHeads = 32 / kLanes, kBatch = 4;  // heads a warp takes at a time; times this
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  constexpr int kWarps = kThreads / 32;
   const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
   const int64_t total = min64(a.st.off[a.st.B], a.st.rows);
   const int64_t r1 = min64(r0 + a.rows_per_cta, total);
   if (r0 >= r1) return;
-  const uint32_t cap = (uint32_t)a.st.width * (uint32_t)a.c.ps;
+  const int64_t cap = (int64_t)a.st.width * a.c.ps;
   int b = kv_sequence_of(a.st, r0);
   int64_t begin = a.st.off[b], end = a.st.off[b + 1], len = a.st.lens[b];
-  int turn = 0;  // jobs go round the warps
-  for (int64_t r = r0; r < r1; ++r) {
+  auto follow = [&](int64_t r) {  // the sequence of a later row; its position
     while (r >= end && b + 1 < a.st.B) {
       ++b;
       begin = end;
       end = a.st.off[b + 1];
       len = a.st.lens[b];
     }
-    const int64_t p64 = len - end + r;
-    if (p64 < 0 || p64 >= (int64_t)cap) continue;
-    const uint32_t p = (uint32_t)p64;
-    if (p % kKvBlock == 0 || r == begin || p == 0) {
-      const uint32_t base = p / kKvBlock * kKvBlock;
+    return len - end + r;
+  };
+  if (blockIdx.y < a.kv_slices) {
+    const int job = (int)blockIdx.y * kWarps + warp;
+    if (job >= 2 * a.c.hk) return;
+    for (int64_t r = r0; r < r1; ++r) {
+      const int64_t p64 = follow(r);
+      if (p64 < 0 || p64 >= cap || (p64 % kKvBlock && r != begin)) continue;
+      const uint32_t p = (uint32_t)p64, base = p / kKvBlock * kKvBlock;
       const uint32_t p1 = (uint32_t)min64(min64((int64_t)base + kKvBlock, len), min64(p64 + (total - r), cap));
       const int page = kv_page(a.st, a.c, b, p);
-      if (page >= 0) {
-        for (int j = 0; j < 2 * a.c.hk; ++j, ++turn)
-          if (turn % kWarps == warp)
-            append_block<D, BF16>(a, j < a.c.hk, j < a.c.hk ? j : j - a.c.hk, page, r, base, p, p1, lane);
-      }
+      if (page >= 0)
+        append_block<D, BF16>(a, job < a.c.hk, job < a.c.hk ? job : job - a.c.hk, page, r, base, p, p1, lane);
     }
-    if (a.q) {  // kRows heads of this row a pass
-      const Turn t = turn_of<D>(a.rot, a.interleaved, lane);
-      for (int h0 = 0; h0 < a.hq; h0 += kRows, ++turn) {
-        if (turn % kWarps != warp) continue;
-        const int h = h0 + lane / kLanes;
-        const bool live = h < a.hq;
-        const int64_t at = (int64_t)h * D + lane % kLanes * kE;
-        float x[kE], y[kE];
+    return;
+  }
+  // A row's heads are one warp's, or, where the rows are few, several warps'.
+  const int split = a.rows_per_cta >= kWarps ? 1 : kWarps / a.rows_per_cta;
+  const int per = ((a.hq + split - 1) / split + kHeads - 1) / kHeads * kHeads;
+  const Turn t = turn_of<D>(a.rot, a.interleaved, lane);
+  for (int64_t r = r0 + warp / split; r < r1; r += kWarps / split) {
+    const int64_t p = follow(r);
+    if (p < 0 || p >= cap) continue;
+    const Angles an = angles_at(t, t.on, a.cos, a.sin, p, a.rot / 2);
+    const int h1 = min(a.hq, (warp % split + 1) * per);
+    for (int h0 = warp % split * per; h0 < h1; h0 += kBatch * kHeads) {
+      float x[kBatch][kE];
 #pragma unroll
-        for (int j = 0; j < kE; ++j) x[j] = 0.f;
-        if (live) load8<BF16>(a.q, r * a.q_stride + at, x);
-        rotate<float>(x, y, t, live, a.cos, a.sin, p, a.rot / 2);
-        if (live) store8<BF16>(a.q_out, r * a.q_out_stride + at, y);
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * kHeads + lane / kLanes;
+#pragma unroll
+        for (int j = 0; j < kE; ++j) x[i][j] = 0.f;
+        if (h < h1) load8<BF16>(a.q, r * a.q_stride + (int64_t)h * D + lane % kLanes * kE, x[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const int h = h0 + i * kHeads + lane / kLanes;
+        rotate(x[i], t, an, turned);
+        if (h < h1) store8<BF16>(a.q_out, r * a.q_out_stride + (int64_t)h * D + lane % kLanes * kE, x[i]);
       }
     }
   }
@@ -300,10 +308,11 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const KvAppendArgs 
 
 cudaError_t launch_kv_append(const KvAppendArgs& args, int sms, cudaStream_t s) {
   KvAppendArgs a = args;
-  int per = kKvBlock;
-  while (per > 1 && (a.st.rows + per - 1) / per < 8 * sms) per /= 2;
+  int per = kKvBlock;  // fewer where that leaves SMs without work
+  while (per > 1 && (a.st.rows + per - 1) / per < 2 * sms) per /= 2;
   a.rows_per_cta = per;
-  const unsigned grid = (unsigned)((a.st.rows + per - 1) / per);
+  a.kv_slices = (2 * a.c.hk + kWarps - 1) / kWarps;
+  const dim3 grid((unsigned)((a.st.rows + per - 1) / per), (unsigned)(a.kv_slices + (a.q ? 1 : 0)));
   if (a.c.d == 128)
     a.is_bf16 ? kv_append_kernel<128, true><<<grid, kThreads, 0, s>>>(a)
               : kv_append_kernel<128, false><<<grid, kThreads, 0, s>>>(a);
