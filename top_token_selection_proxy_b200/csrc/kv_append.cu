@@ -7,7 +7,7 @@
 // rounded once, and rounding held values again changes only those that leave e4m3's normal range.
 //
 // What bounds it: bytes (a key row is read once at 2 or 4 bytes an element and written at 1, a query row is read
-// and written).  A block is one warp's work for one head and one of k and v: its (up to 16) token rows stay in
+// and written).  A block is two warps' work for one head and one of k and v: its (up to 16) token rows stay in
 // registers between the maximum and the rounding, so nothing is read twice; 8 elements a lane, 16-byte loads.
 // Query rows are other CTAs' work: a warp keeps a row's angles and takes its heads in batches of loads.
 #include "kv.cuh"
@@ -18,20 +18,36 @@ namespace {
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kE = 8;  // elements a lane holds of a row
 
+// 8 elements as they lie in memory, and as fp32.
 template <bool BF16>
-__device__ __forceinline__ void load8(const void* p, int64_t at, float (&x)[kE]) {
-  if (BF16) {
-    const uint4 r = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p) + at);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
+struct Raw {
+  uint4 v[BF16 ? 1 : 2];
+};
+
+template <bool BF16>
+__device__ __forceinline__ Raw<BF16> load8(const void* p, int64_t at, bool live) {
+  Raw<BF16> r;
+  const uint4* src = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + at * (BF16 ? 2 : 4));
+#pragma unroll
+  for (int i = 0; i < (BF16 ? 1 : 2); ++i) r.v[i] = live ? src[i] : make_uint4(0, 0, 0, 0);
+  return r;
+}
+
+template <bool BF16>
+__device__ __forceinline__ void widen(const Raw<BF16>& r, float (&x)[kE]) {
+  if constexpr (BF16) {
+    const uint32_t w[4] = {r.v[0].x, r.v[0].y, r.v[0].z, r.v[0].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       x[2 * i] = __uint_as_float(w[i] << 16);
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   } else {
-    const float4* f = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(p) + at);
-    const float4 a = f[0], b = f[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      x[4 * i] = __uint_as_float(r.v[i].x), x[4 * i + 1] = __uint_as_float(r.v[i].y);
+      x[4 * i + 2] = __uint_as_float(r.v[i].z), x[4 * i + 3] = __uint_as_float(r.v[i].w);
+    }
   }
 }
 
@@ -103,40 +119,50 @@ __device__ __forceinline__ Angles angles_at(const Turn& t, bool go, const float*
       const float4 c1 = __ldg(pc + 1), s1 = __ldg(ps + 1);
       a.c[4] = c1.x, a.c[5] = c1.y, a.c[6] = c1.z, a.c[7] = c1.w;
       a.s[4] = s1.x, a.s[5] = s1.y, a.s[6] = s1.z, a.s[7] = s1.w;
+#pragma unroll
+      for (int i = 0; i < kE; ++i) a.s[i] *= t.sign;  // the lower half's pairs take -sin
     }
   }
   return a;
 }
 
 // a c + b s in fp32.
-__device__ __forceinline__ float turned(float a, float c, float b, float s) { return fmaf(b, s, a * c); }
+struct Turned {
+  __device__ float operator()(float a, float c, float b, float s) const { return fmaf(b, s, a * c); }
+};
 
 // a c + b s rounded to odd at 24 bits: the exact value's neighbour whose last bit is set, unless it is exact.  A
 // later rounding to fewer bits, and a comparison with a power of two times 448, then give what the exact value
 // gives.  The products' and the sum's own errors are exact fp32 values (fused multiply-add; Knuth's two-sum).
-__device__ __forceinline__ float turned_odd(float a, float c, float b, float s) {
-  const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
-  const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
-  const float sum = __fadd_rn(p, q), v = __fsub_rn(sum, p);
-  const float es = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, v)), __fsub_rn(q, v));
-  const float low = __fadd_rn(es, __fadd_rn(ep, eq));
-  const float hi = __fadd_rn(sum, low);
-  const float rest = __fsub_rn(low, __fsub_rn(hi, sum));
-  const int bits = __float_as_int(hi);
-  if ((rest > 0.f || rest < 0.f) && !(bits & 1)) return __int_as_float((rest > 0.f) == (hi > 0.f) ? bits + 1 : bits - 1);
-  return hi;  // exact, odd already, or not finite
-}
+struct TurnedOdd {
+  __device__ float operator()(float a, float c, float b, float s) const {
+    const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);
+    const float ep = __fmaf_rn(a, c, -p), eq = __fmaf_rn(b, s, -q);
+    const float sum = __fadd_rn(p, q), v = __fsub_rn(sum, p);
+    const float es = __fadd_rn(__fsub_rn(p, __fsub_rn(sum, v)), __fsub_rn(q, v));
+    const float low = __fadd_rn(es, __fadd_rn(ep, eq));
+    const float hi = __fadd_rn(sum, low);
+    const float rest = __fsub_rn(low, __fsub_rn(hi, sum));
+    const int bits = __float_as_int(hi);
+    if ((rest > 0.f || rest < 0.f) && !(bits & 1)) return __int_as_float((rest > 0.f) == (hi > 0.f) ? bits + 1 : bits - 1);
+    return hi;  // exact, odd already, or not finite
+  }
+};
 
-// x turned: F(a, c, b, s) forms each element.  All lanes of the warp take part.
-template <typename F>
-__device__ __forceinline__ void rotate(float (&x)[kE], const Turn& t, const Angles& a, F form) {
+// The elements of r, turned: form(a, c, b, s) = a c + b s.  All lanes of the warp take part.
+template <bool BF16, typename F>
+__device__ __forceinline__ void rotate(const Raw<BF16>& r, float (&x)[kE], const Turn& t, const Angles& a, F form) {
+  widen<BF16>(r, x);
   if (t.split) {
-    const float sign = t.on ? t.sign : 0.f;
+    Raw<BF16> other;  // exchanged as it lies in memory: two bf16 a word
+    float y[kE];
 #pragma unroll
-    for (int i = 0; i < kE; ++i) {
-      const float other = __shfl_sync(~0u, x[i], t.peer);
-      x[i] = t.on ? form(x[i], a.c[i], other, sign * a.s[i]) : x[i];
-    }
+    for (int i = 0; i < (BF16 ? 1 : 2); ++i)
+      other.v[i] = make_uint4(__shfl_sync(~0u, r.v[i].x, t.peer), __shfl_sync(~0u, r.v[i].y, t.peer),
+                              __shfl_sync(~0u, r.v[i].z, t.peer), __shfl_sync(~0u, r.v[i].w, t.peer));
+    widen<BF16>(other, y);
+#pragma unroll
+    for (int i = 0; i < kE; ++i) x[i] = t.on ? form(x[i], a.c[i], y[i], a.s[i]) : x[i];
   } else if (t.on) {
 #pragma unroll
     for (int i = 0; i < kE / 2; ++i) {
@@ -165,62 +191,73 @@ __device__ __forceinline__ float finite_abs(float y) {
   return a <= 3.402823466e38f ? a : 0.f;  // NaN and infinities do not set the scale
 }
 
-// One block of one sequence and head: new tokens [p0, p1) at rows row0 .., earlier ones [base, p0).
+// What the two warps of a block tell each other: the largest value of each half.  One set for each block in turn
+// of two, so that one barrier a block is enough.
+struct Pair {
+  float amax[2][2];
+};
+
+// One block of one sequence and head, by two warps of 8 tokens each: new tokens [p0, p1) at rows row0 .., earlier
+// ones [base, p0).  `half`: which of the two this warp is.
 template <int D, bool BF16>
-__device__ void append_block(const KvAppendArgs& a, bool is_key, int head, int page, int64_t row0, uint32_t base,
-                             uint32_t p0, uint32_t p1, int lane) {
-  constexpr int kLanes = D / kE, kRows = 32 / kLanes, kPasses = kKvBlock / kRows;
-  const int sub = lane % kLanes, slot = lane / kLanes;
+__device__ __forceinline__ void append_block(const KvAppendArgs& a, Pair& pair, int bar, int turn, bool is_key, int head, int b,
+                             int64_t row0, uint32_t base, uint32_t p0, uint32_t p1, int half, int lane) {
+  constexpr int kLanes = D / kE, kRows = 32 / kLanes, kPasses = kKvBlock / 2 / kRows;
+  const int sub = lane % kLanes, slot = half * (kKvBlock / 2) + lane / kLanes;
   const void* src = is_key ? a.k : a.v;
   const int64_t stride = is_key ? a.k_stride : a.v_stride;
   const int rot = is_key ? a.rot : 0;
   const Turn t = turn_of<D>(rot, a.interleaved, lane);
-  float y[kPasses][kE];
-  float amax = 0.f;
+  const int page = kv_page(a.st, a.c, b, p0);  // not needed before the rows have come
+  Raw<BF16> raw[kPasses];
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {  // all loads first: they are independent
     const uint32_t p = base + i * kRows + slot;
-    if (p >= p0 && p < p1) {
-      load8<BF16>(src, (row0 + (p - p0)) * stride + head * D + sub * kE, y[i]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < kE; ++j) y[i][j] = 0.f;
-    }
+    raw[i] = load8<BF16>(src, (row0 + (p - p0)) * stride + head * D + sub * kE, p >= p0 && p < p1);
   }
+  float y[kPasses][kE], amax = 0.f;
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const uint32_t p = base + i * kRows + slot;
-    if (rot)
-      rotate(y[i], t, angles_at(t, t.on && p >= p0 && p < p1, a.cos, a.sin, p, a.rot / 2), turned_odd);
+    if (rot) rotate<BF16>(raw[i], y[i], t, angles_at(t, t.on && p >= p0 && p < p1, a.cos, a.sin, p, a.rot / 2), TurnedOdd{});
+    else widen<BF16>(raw[i], y[i]);
 #pragma unroll
-    for (int j = 0; j < kE; ++j) amax = fmaxf(amax, finite_abs(y[i][j]));
+    for (int j = 0; j < kE; ++j) amax = fmaxf(amax, fabsf(y[i][j]));  // passes over NaN
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  int e = exponent_of(amax);
-  uint8_t* dst = is_key ? a.c.k : a.c.v;
-  int8_t* exps = is_key ? a.c.ke : a.c.ve;
-  const int64_t ph = (int64_t)page * a.c.hk + head;
+  if (!(amax <= 3.402823466e38f)) {  // infinities do not set the scale
+    amax = 0.f;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i)
+#pragma unroll
+      for (int j = 0; j < kE; ++j) amax = fmaxf(amax, finite_abs(y[i][j]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
+  }
+  const int64_t ph = (int64_t)max(page, 0) * a.c.hk + head;
   const int in_page = base % (uint32_t)a.c.ps;
-  int8_t* exp_at = exps + ph * (a.c.ps / kKvBlock) + in_page / kKvBlock;
-  uint8_t* rows = dst + (ph * a.c.ps + in_page) * D;
-  if (p0 > base) {  // earlier tokens of the sequence: their exponent, and their payload at the new one
-    const int was = *exp_at;
-    if (was >= e) {
-      e = was;
-    } else {
-      const float f = was - e < -126 ? 0.f : kv_exp2i(was - e);
+  int8_t* exp_at = (is_key ? a.c.ke : a.c.ve) + ph * (a.c.ps / kKvBlock) + in_page / kKvBlock;
+  const bool held = p0 > base;  // earlier tokens of the sequence: their exponent may be the larger
+  const int was = held && page >= 0 ? *exp_at : 0;
+  if (lane == 0) pair.amax[turn & 1][half] = amax;
+  named_bar_sync(bar, 64);  // both halves' maxima; and both have read the exponent
+  int e = exponent_of(fmaxf(pair.amax[turn & 1][0], pair.amax[turn & 1][1]));
+  if (page < 0) return;
+  uint8_t* rows = (is_key ? a.c.k : a.c.v) + (ph * a.c.ps + in_page) * D;
+  if (held && was >= e) e = was;
+  if (held && was < e) {  // their payload at the new scale
+    const float f = was - e < -126 ? 0.f : kv_exp2i(was - e);
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i) {
-        const uint32_t p = base + i * kRows + slot;
-        if (p < p0) {
-          uint2* at = reinterpret_cast<uint2*>(rows + (int64_t)(p - base) * D + sub * kE);
-          const uint2 r = *at;
-          float z[kE];
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t p = base + i * kRows + slot;
+      if (p < p0) {
+        uint2* at = reinterpret_cast<uint2*>(rows + (int64_t)(p - base) * D + sub * kE);
+        const uint2 r = *at;
+        float z[kE];
 #pragma unroll
-          for (int j = 0; j < kE; ++j) z[j] = kv_e4m3_to_f32((uint8_t)((j < 4 ? r.x : r.y) >> (8 * (j & 3)))) * f;
-          *at = make_uint2(pack4(z[0], z[1], z[2], z[3]), pack4(z[4], z[5], z[6], z[7]));
-        }
+        for (int j = 0; j < kE; ++j) z[j] = kv_e4m3_to_f32((uint8_t)((j < 4 ? r.x : r.y) >> (8 * (j & 3)))) * f;
+        *at = make_uint2(pack4(z[0], z[1], z[2], z[3]), pack4(z[4], z[5], z[6], z[7]));
       }
     }
   }
@@ -228,23 +265,22 @@ __device__ void append_block(const KvAppendArgs& a, bool is_key, int head, int p
 #pragma unroll
   for (int i = 0; i < kPasses; ++i) {
     const uint32_t p = base + i * kRows + slot;
-    if (p >= p0 && p < p1) {
-      const float(&z)[kE] = y[i];
+    const float(&z)[kE] = y[i];
+    if (p >= p0 && p < p1)
       *reinterpret_cast<uint2*>(rows + (int64_t)(p - base) * D + sub * kE) =
           make_uint2(pack4(z[0] * inv, z[1] * inv, z[2] * inv, z[3] * inv),
                      pack4(z[4] * inv, z[5] * inv, z[6] * inv, z[7] * inv));
-    }
   }
-  __syncwarp();  // every lane has read the old exponent
-  if (lane == 0) *exp_at = (int8_t)e;
+  if (lane == 0 && half == 0) *exp_at = (int8_t)e;
 }
 
 // A CTA takes `rows_per_cta` rows.  The first `kv_slices` of each such group append the blocks whose first new token
-// is among them (a block's other rows may follow behind), a warp for each of 8 of the heads of k and v; the others
-// rotate the query rows.
+// is among them (a block's other rows may follow behind), two warps for each of 4 of the heads of k and v; the
+// others rotate the query rows.
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kThreads, 2) kv_append_kernel(const KvAppendArgs a) {
-  constexpr int kLanes = D / kE, kHeads = 32 / kLanes, kBatch = 4;  // heads a warp takes at a time; times this
+__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_append_kernel(const KvAppendArgs a) {
+  constexpr int kLanes = D / kE, kHeads = 32 / kLanes;  // heads a warp takes at a time
+  constexpr int kBatch = 8;                 // ... and loads of them under way
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int64_t r0 = (int64_t)blockIdx.x * a.rows_per_cta;
   const int64_t total = min64(a.st.off[a.st.B], a.st.rows);
@@ -263,16 +299,21 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_kernel(const KvAppendAr
     return len - end + r;
   };
   if (blockIdx.y < a.kv_slices) {
-    const int job = (int)blockIdx.y * kWarps + warp;
+    __shared__ Pair pairs[kWarps / 2];
+    const int job = (int)blockIdx.y * (kWarps / 2) + warp / 2;
     if (job >= 2 * a.c.hk) return;
-    for (int64_t r = r0; r < r1; ++r) {
+    int turn = 0;
+    for (int64_t r = r0; r < r1;) {
       const int64_t p64 = follow(r);
-      if (p64 < 0 || p64 >= cap || (p64 % kKvBlock && r != begin)) continue;
-      const uint32_t p = (uint32_t)p64, base = p / kKvBlock * kKvBlock;
-      const uint32_t p1 = (uint32_t)min64(min64((int64_t)base + kKvBlock, len), min64(p64 + (total - r), cap));
-      const int page = kv_page(a.st, a.c, b, p);
-      if (page >= 0)
-        append_block<D, BF16>(a, job < a.c.hk, job < a.c.hk ? job : job - a.c.hk, page, r, base, p, p1, lane);
+      const int in = (int)p64 & (kKvBlock - 1);
+      const int64_t next = p64 < 0 ? r - p64 : p64 < cap ? r + kKvBlock - in : end;  // row of the next block's first token
+      if (p64 >= 0 && p64 < cap && (in == 0 || r == begin)) {
+        const uint32_t p = (uint32_t)p64, base = p - in;
+        const uint32_t p1 = (uint32_t)min64(min64((int64_t)base + kKvBlock, len), min64(p64 + (total - r), cap));
+        append_block<D, BF16>(a, pairs[warp / 2], 1 + warp / 2, turn++, job < a.c.hk,
+                              job < a.c.hk ? job : job - a.c.hk, b, r, base, p, p1, warp & 1, lane);
+      }
+      r = max64(min64(next, end), r + 1);
     }
     return;
   }
@@ -285,20 +326,17 @@ __global__ void __launch_bounds__(kThreads, 2) kv_append_kernel(const KvAppendAr
     if (p < 0 || p >= cap) continue;
     const Angles an = angles_at(t, t.on, a.cos, a.sin, p, a.rot / 2);
     const int h1 = min(a.hq, (warp % split + 1) * per);
-    for (int h0 = warp % split * per; h0 < h1; h0 += kBatch * kHeads) {
-      float x[kBatch][kE];
+    for (int h0 = warp % split * per + lane / kLanes; h0 - lane / kLanes < h1; h0 += kBatch * kHeads) {
+      Raw<BF16> raw[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        raw[i] = load8<BF16>(a.q, r * a.q_stride + (int64_t)(h0 + i * kHeads) * D + lane % kLanes * kE, h0 + i * kHeads < h1);
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * kHeads + lane / kLanes;
-#pragma unroll
-        for (int j = 0; j < kE; ++j) x[i][j] = 0.f;
-        if (h < h1) load8<BF16>(a.q, r * a.q_stride + (int64_t)h * D + lane % kLanes * kE, x[i]);
-      }
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int h = h0 + i * kHeads + lane / kLanes;
-        rotate(x[i], t, an, turned);
-        if (h < h1) store8<BF16>(a.q_out, r * a.q_out_stride + (int64_t)h * D + lane % kLanes * kE, x[i]);
+        float x[kE];
+        rotate<BF16>(raw[i], x, t, an, Turned{});
+        if (h0 + i * kHeads < h1)
+          store8<BF16>(a.q_out, r * a.q_out_stride + (int64_t)(h0 + i * kHeads) * D + lane % kLanes * kE, x);
       }
     }
   }
@@ -311,7 +349,7 @@ cudaError_t launch_kv_append(const KvAppendArgs& args, int sms, cudaStream_t s) 
   int per = kKvBlock;  // fewer where that leaves SMs without work
   while (per > 1 && (a.st.rows + per - 1) / per < 2 * sms) per /= 2;
   a.rows_per_cta = per;
-  a.kv_slices = (2 * a.c.hk + kWarps - 1) / kWarps;
+  a.kv_slices = (2 * a.c.hk + kWarps / 2 - 1) / (kWarps / 2);
   const dim3 grid((unsigned)((a.st.rows + per - 1) / per), (unsigned)(a.kv_slices + (a.q ? 1 : 0)));
   if (a.c.d == 128)
     a.is_bf16 ? kv_append_kernel<128, true><<<grid, kThreads, 0, s>>>(a)
