@@ -61,10 +61,15 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, int sms, cudaStream_t s);
 // What a CTA leaves for the merge when it began an item that others end.  The work of an attention call is a line
 // of tiles, item after item, of which every CTA takes an equal stretch.
 struct alignas(16) KvOpen {
-  int64_t item_end, total;  // in tiles of the line
-  int64_t row0;             // first query row's index
-  int32_t stretch, cta_count, head0, rr0, valid, open;
+  int64_t row0;                            // first query row's index
+  int32_t stretch, head0, rr0, valid, open;  // open: how many CTAs' results make the item (0: none was begun)
 };
+
+// The CTA after the last one whose stretch reaches into an item that ends at `item_end`: stretch j begins at
+// total * j / ctas.
+__device__ __forceinline__ int kv_parts(int64_t item_end, int64_t total, int64_t ctas) {
+  return (int)((item_end * ctas + total - 1) / total);
+}
 
 struct KvLine {
   int* status;
@@ -92,7 +97,7 @@ cudaError_t kv_allow_smem(size_t bytes) {
 
 size_t kv_attn_workspace(int sms, int d);
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, const int* gate, cudaStream_t s);
-cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, int split, float lift,
+cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, bool many, float lift,
                             cudaStream_t s);
 size_t kv_attn_tc_workspace(int sms, int d);
 cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms, void* ws,

@@ -25,7 +25,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRowsT = 16;              // query rows of an item
 constexpr int kWTok = 32;               // tokens a warp takes at a time (two blocks)
 constexpr int kTile = kWTok * kWarps;   // tokens of a tile
-constexpr float kLift = 14.f;           // weights stand 2^14 above the largest term: fp16 keeps 11 bits down to 2^-28
+constexpr float kLift = 2.f, kSlack = 13.f;  // weights up to 2^15: the maxima may lag by 2^13 before sums are rescaled
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -186,7 +186,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
     const int64_t p_lo = first + rr0 / a.group, p_hi = first + (rr0 + valid - 1) / a.group;
     const int64_t pr[2] = {first + (rr0 + min(g, valid - 1)) / a.group, first + (rr0 + min(g + 8, valid - 1)) / a.group};
 
-    // q: this lane's operands, scaled by a power of two so that the row's largest lies in [2^14, 2^15)
+    // q: this lane's operands, scaled by a power of two so that the row's largest lies in [2^14, 2^15): one fp16 holds
+    // a bf16's 8 bits (down to 2^-31 of the largest), three hold an fp32's 24.
     uint32_t qa[BF16 ? NK : 1][4];
     float unit[2];  // scale2 / that power
     {
@@ -221,19 +222,22 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
             }
           }
         top = quad_max(top);
-        const int ex = top > 0.f && top <= 3.402823466e38f ? max((int)(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
+        const bool finite = top <= 3.402823466e38f;
+        const int ex = top > 0.f && finite ? max((int)(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
         unit[i] = a.scale2 * kv_exp2i(ex);
         const float down = kv_exp2i(-ex);
 #pragma unroll
         for (int k = 0; k < D / 4; ++k) v[i][k] *= down;
       }
+      if (BF16) {
 #pragma unroll
-      for (int ks = 0; ks < NK; ++ks) {
-        if (BF16) {
+        for (int ks = 0; ks < NK; ++ks)
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // a0: row g, a1: row g + 8, a2, a3: the same rows' next two dims
-            qa[ks][k] = pack_f16(v[k & 1][4 * ks + (k & 2)], v[k & 1][4 * ks + (k & 2) + 1]);
-        } else if (warp == 0) {  // fp32: three fp16 parts hold all 24 bits; kept in shared memory
+            qa[BF16 ? ks : 0][k] = pack_f16(v[k & 1][4 * ks + (k & 2)], v[k & 1][4 * ks + (k & 2) + 1]);
+      } else if (warp == 0) {  // kept in shared memory
+#pragma unroll
+        for (int ks = 0; ks < NK; ++ks)
 #pragma unroll
           for (int part = 0; part < S::kQParts; ++part) {
             uint32_t w[4];
@@ -247,12 +251,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
             }
             qs[(part * NK + ks) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
           }
-        }
       }
       if (!BF16) __syncthreads();
     }
 
-    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, mp[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, mp[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, back[2] = {1.f, 1.f};
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
@@ -291,7 +294,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       if (s < 0 || s > hi) return -1;
       return kv_page(a.st, a.c, b, (uint32_t)s);
     };
-    // the copies of one step; returns the lane's token's packed (ke, ve) with bit 16 set where it is present
+    // the copies of one step; returns the lane's token's scales: ke + 127 in the low byte, ve as bf16 in the upper
+    // half; 0 where it is absent
     auto issue = [&](int step, int s, int page) -> uint32_t {
       uint32_t ex = 0;
       if (step < steps) {
@@ -300,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
         const int slot = page >= 0 ? (page * a.c.hk + h) * a.c.ps + (int)in : -1;  // row of the cache
         if (page >= 0) {
           const int64_t be = ((int64_t)page * a.c.hk + h) * (a.c.ps / kKvBlock) + in / kKvBlock;
-          ex = (uint8_t)__ldg(a.c.ke + be) | ((uint32_t)(uint8_t)__ldg(a.c.ve + be) << 8) | 0x10000u;
+          ex = (uint32_t)(max((int)__ldg(a.c.ke + be), -126) + 127) | __float_as_uint((float)__ldg(a.c.ve + be));
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -380,10 +384,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 
       // scale, mask
       float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
-      uint32_t te[4][2];  // (ke, ve, present) of the two tokens that this lane holds in each tile
-      bool part_seen = false;  // some row sees a token of this step that another does not
-      const bool whole = !SEL && __all_sync(~0u, ex >> 16) && base + kWTok - 1 <= min64(p_lo, hi) &&
-                         (a.window <= 0 || base > p_hi - a.window || base + kWTok <= a.sinks);
+      uint32_t te[4][2];  // scales of the two tokens that this lane holds in each tile
+      const bool whole = __all_sync(~0u, ex != 0) &&
+                         (SEL || (base + kWTok - 1 <= min64(p_lo, hi) &&
+                                  (a.window <= 0 || base > p_hi - a.window || base + kWTok <= a.sinks)));
       if (SEL) {
 #pragma unroll
         for (int j = 0; j < 4; ++j)
@@ -400,68 +404,91 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       for (int j = 0; j < 4; ++j)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float ks = kv_scale((int8_t)te[j][k]);
-          const float ve = (float)(int8_t)(te[j][k] >> 8);
-          const int s = base + 8 * j + 2 * tig + k;
+          const float ks = __uint_as_float(te[j][k] << 23);
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            float v = z[j][2 * i + k] * (unit[i] * ks);
-            if (SEL) {
-              if (!(te[j][k] >> 16)) v = -INFINITY;
-            } else if (!whole) {
-              const bool seen = (te[j][k] >> 16) && s <= hi && s <= pr[i] &&
-                                (a.window <= 0 || s > pr[i] - a.window || s < a.sinks);
-              if (!seen) v = -INFINITY;
+          for (int i = 0; i < 2; ++i) z[j][2 * i + k] *= unit[i] * ks;
+        }
+      if (!whole) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int s = base + 8 * j + 2 * tig + k;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const bool seen = te[j][k] && (SEL || (s <= hi && s <= pr[i] &&
+                                                     (a.window <= 0 || s > pr[i] - a.window || s < a.sinks)));
+              if (!seen) z[j][2 * i + k] = -INFINITY;
             }
-            z[j][2 * i + k] = v;
-            top[i] = fmaxf(top[i], v);
-            topv[i] = fmaxf(topv[i], v + ve);
           }
-        }
-      if (!SEL && !whole) part_seen = true;
-
-      // the running maxima
-      float lift[2];
-      bool moved = false;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const float mn = fmaxf(m[i], quad_max(top[i])), mpn = fmaxf(mp[i], quad_max(topv[i]));
-        moved |= mpn != mp[i];
-        top[i] = mpn;
-        if (mn != m[i]) l[i] *= ex2(m[i] - mn);
-        m[i] = mn;
-        lift[i] = mn == -INFINITY ? 0.f : mn;
       }
-      if (__any_sync(~0u, moved)) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float f = top[i] == mp[i] ? 1.f : ex2(mp[i] - top[i]);
-          mp[i] = top[i];
-#pragma unroll
-          for (int n8 = 0; n8 < NT; ++n8) o[n8][2 * i] *= f, o[n8][2 * i + 1] *= f;
-        }
-      }
-      // weights: p for the sum, p * 2^(ve + m - m' + 14) for the product
-      uint32_t pa[2][4], pb[2][4];  // operands of the two blocks; the rest of them (fp32)
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float off = lift[i] - (mp[i] == -INFINITY ? 0.f : mp[i]) + kLift;
-          float w[2];
+        for (int k = 0; k < 2; ++k) {
+          const float ve = __uint_as_float(te[j][k] & 0xFFFF0000u);
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {
+          for (int i = 0; i < 2; ++i) {
+            top[i] = fmaxf(top[i], z[j][2 * i + k]);
+            topv[i] = fmaxf(topv[i], z[j][2 * i + k] + ve);
+          }
+        }
+      // some row sees a token of this step that another does not
+      const bool part_seen = !SEL && !whole;
+
+      // the running maxima, which may lag; the four lanes of a row hold the same
+      bool up = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) up |= top[i] > m[i] + kSlack || topv[i] > mp[i] + kSlack;
+      if (__any_sync(~0u, up)) {
+        bool scaled = false;
+        float f[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float mn = quad_max(top[i]), mpn = quad_max(topv[i]);
+          if (mn > m[i] + kSlack) {
+            if (m[i] != -INFINITY) l[i] *= ex2(m[i] - mn);
+            m[i] = mn;
+          }
+          f[i] = 1.f;
+          if (mpn > mp[i] + kSlack) {
+            if (mp[i] != -INFINITY) f[i] = ex2(mp[i] - mpn);
+            mp[i] = mpn;
+          }
+          scaled |= f[i] != 1.f;
+          back[i] = ex2((m[i] == -INFINITY ? 0.f : m[i]) - (mp[i] == -INFINITY ? 0.f : mp[i]) + kLift);
+        }
+        if (__any_sync(~0u, scaled)) {
+#pragma unroll
+          for (int n8 = 0; n8 < NT; ++n8) o[n8][0] *= f[0], o[n8][1] *= f[0], o[n8][2] *= f[1], o[n8][3] *= f[1];
+        }
+      }
+      // weights: p for the sum, p * 2^(m - m' + 2) * 2^ve for the product
+      uint32_t pa[2][4], pb[2][4];  // operands of the two blocks; the rest of them (fp32)
+      const float lift[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        float w[2][2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float vs = ex2(__uint_as_float(te[j][k] & 0xFFFF0000u));
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
             const float p = ex2(z[j][2 * i + k] - lift[i]);
             l[i] += p;
-            w[k] = p * ex2(fminf((float)(int8_t)(te[j][k] >> 8) + off, 126.f));  // finite: p may be a masked zero
+            w[i][k] = p * back[i] * vs;
           }
-          const uint32_t hw = pack_f16(w[0], w[1]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t hw = pack_f16(w[i][0], w[i][1]);
           pa[j / 2][2 * (j % 2) + i] = hw;
           if (!BF16) {
             const __half2 hh = *reinterpret_cast<const __half2*>(&hw);
-            pb[j / 2][2 * (j % 2) + i] = pack_f16(w[0] - __low2float(hh), w[1] - __high2float(hh));
+            pb[j / 2][2 * (j % 2) + i] = pack_f16(w[i][0] - __low2float(hh), w[i][1] - __high2float(hh));
           }
         }
+      }
 
       // output sums: 16 tokens a block, NT tiles of 8 dims
       constexpr int VW = S::kVBytes / 4;  // words a lane holds of a value
@@ -608,7 +635,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       }
     }
     if (!all && t0 == 0 && tid == 0)
-      *open = {at - t0 + e.tiles, total, row0, (int)blockIdx.x, (int)ctas, h * a.group, rr0, valid, 1};
+      *open = {row0, (int)blockIdx.x, h * a.group, rr0, valid, kv_parts(at - t0 + e.tiles, total, ctas) - (int)blockIdx.x};
     __syncthreads();  // the ring is free again
 
     at += t1 - t0;
@@ -628,81 +655,65 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   }
 }
 
-// Joins the partial results of an item that several CTAs worked on: block (c, y) those that CTA c began.  Warps take
-// every eighth of them, lanes four dims; the order of the sums is fixed by the line alone.
+// Joins the partial results of an item that several CTAs worked on: blocks (c, y) those that CTA c began.  `per_row`
+// warps take one of the item's rows together, lanes four dims; the order of the sums is fixed by the line alone.
 constexpr int kMergeWarps = 8;
 template <int D, bool BF16>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-    kv_merge_kernel(const KvAttnArgs a, const KvLine line, const int rows, const float lift) {
+    kv_merge_kernel(const KvAttnArgs a, const KvLine line, const int rows, const float lift, const int per_row) {
   __shared__ float sums[kMergeWarps][D + 4];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (line.gate && *line.gate == 0) return;
   const KvOpen op = line.open[blockIdx.x];
   if (!op.open) return;
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-  // CTAs c + 1 .. c + more work on the item's other tiles
-  int more = 0;
-  {
-    int64_t lo = op.stretch, hi = op.cta_count;  // begin(lo) < item_end <= begin(hi)
-    while (hi - lo > 1) {
-      const int64_t mid = (lo + hi) >> 1;
-      if (op.total * mid / op.cta_count < op.item_end) lo = mid;
-      else hi = mid;
-    }
-    more = (int)(lo - op.stretch);
-  }
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, sub = warp % per_row;
+  const int more = op.open - 1;  // CTAs c + 1 .. c + more work on the item's other tiles
+  const int r = blockIdx.y * (kMergeWarps / per_row) + warp / per_row;
+  if (per_row == 1 && r >= op.valid) return;
   auto part_of = [&](int i) {  // the first one stands in the place of an item begun, the others in that of one ended
     return line.part + ((int64_t)(op.stretch + i) * 2 + (i == 0)) * kv_part_floats(rows, D);
   };
-  for (int r = blockIdx.y; r < op.valid; r += gridDim.y) {
-    float mp = -INFINITY, m = -INFINITY;
-    for (int i = lane; i <= more; i += 32) {
-      const float4 s = *reinterpret_cast<const float4*>(part_of(i) + rows * D + r * 4);
-      mp = fmaxf(mp, s.x);
-      m = fmaxf(m, s.y);
-    }
+  const int64_t stat_at = (int64_t)rows * D + (int64_t)min(r, rows - 1) * 4;
+  float mp = -INFINITY, m = -INFINITY;
+  for (int i = lane; i <= more; i += 32) {
+    const float4 s = *reinterpret_cast<const float4*>(part_of(i) + stat_at);
+    mp = fmaxf(mp, s.x);
+    m = fmaxf(m, s.y);
+  }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      mp = fmaxf(mp, __shfl_xor_sync(~0u, mp, o));
-      m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-    }
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    const bool mine = lane * 4 < D;
+  for (int o = 16; o; o >>= 1) {
+    mp = fmaxf(mp, __shfl_xor_sync(~0u, mp, o));
+    m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+  }
+  float l = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const bool mine = lane * 4 < D && r < op.valid;
 #pragma unroll 4
-    for (int i = warp; i <= more; i += kMergeWarps) {
-      const float* p = part_of(i);
-      const float4 s = *reinterpret_cast<const float4*>(p + rows * D + r * 4);
-      l += s.y == -INFINITY ? s.z : s.z * ex2(s.y - m);
-      const float f = s.x == -INFINITY ? (s.z == 0.f ? 0.f : 1.f) : ex2(s.x - mp);
-      if (mine) {
-        const float4 v = *reinterpret_cast<const float4*>(p + r * D + lane * 4);
-        acc.x += f == 0.f ? 0.f : v.x * f, acc.y += f == 0.f ? 0.f : v.y * f;
-        acc.z += f == 0.f ? 0.f : v.z * f, acc.w += f == 0.f ? 0.f : v.w * f;
-      }
-    }
-    if (mine) *reinterpret_cast<float4*>(&sums[warp][lane * 4]) = acc;
+  for (int i = sub; i <= more; i += per_row) {
+    const float* p = part_of(i);
+    const float4 s = *reinterpret_cast<const float4*>(p + stat_at);
+    const float4 v = mine ? *reinterpret_cast<const float4*>(p + r * D + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    l += s.y == -INFINITY ? s.z : s.z * ex2(s.y - m);
+    const float f = s.x == -INFINITY ? (s.z == 0.f ? 0.f : 1.f) : ex2(s.x - mp);
+    if (f != 0.f) acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+  }
+  if (per_row > 1) {
+    if (lane * 4 < D) *reinterpret_cast<float4*>(&sums[warp][lane * 4]) = acc;
     if (lane == 0) sums[warp][D] = l;
     __syncthreads();
-    if (warp == 0) {
-      float lt = 0.f;
-      acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kMergeWarps; ++w) {
-        lt += sums[w][D];
-        if (mine) acc.x += sums[w][lane * 4], acc.y += sums[w][lane * 4 + 1], acc.z += sums[w][lane * 4 + 2],
-                  acc.w += sums[w][lane * 4 + 3];
-      }
-      const int64_t row = op.row0 + (op.rr0 + r) / a.group;
-      if (row < a.st.rows) {
-        const int j = op.head0 + (op.rr0 + r) % a.group;
-        const float f = lt == 0.f ? 0.f : ex2(mp - m - lift) / lt;
-        if (mine) kv_store4(a, (row * a.hq + j) * (int64_t)D + lane * 4, acc.x * f, acc.y * f, acc.z * f, acc.w * f, BF16);
-        if (a.lse && lane == 0) a.lse[row * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(lt));
-      }
+    if (sub) return;
+    for (int w = 1; w < per_row; ++w) {
+      l += sums[warp + w][D];
+      if (lane * 4 < D) acc.x += sums[warp + w][lane * 4], acc.y += sums[warp + w][lane * 4 + 1],
+                        acc.z += sums[warp + w][lane * 4 + 2], acc.w += sums[warp + w][lane * 4 + 3];
     }
-    __syncthreads();
   }
+  const int64_t row = op.row0 + (op.rr0 + r) / a.group;
+  if (r >= op.valid || row >= a.st.rows) return;
+  const int j = op.head0 + (op.rr0 + r) % a.group;
+  const float f = l == 0.f ? 0.f : ex2(mp - m - lift) / l;
+  if (mine) kv_store4(a, (row * a.hq + j) * (int64_t)D + lane * 4, acc.x * f, acc.y * f, acc.z * f, acc.w * f, BF16);
+  if (a.lse && lane == 0) a.lse[row * a.hq + j] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
 }
 
 // CTAs of the line: as many as the device holds at once, but no more than there can be tiles.
@@ -736,9 +747,9 @@ cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaS
   kv_attn_kernel<D, BF16, SEL><<<ctas, kThreads, Sh::kBytes, s>>>(a, line);
   e = cudaGetLastError();
   if (e != cudaSuccess || ctas == 1) return e;
-  // Few items cut into many parts: one block for each row of an item, so that a long join has 16 of them.
+  // Few items cut into many parts: all warps of a block for a row; else a warp.
   const int64_t items = a.indices ? a.st.rows * a.c.hk : (a.st.B + a.st.rows * a.group / kRowsT) * (int64_t)a.c.hk;
-  return launch_kv_merge(a, line, ctas, kRowsT, ctas > 4 * items ? kRowsT : 2, kLift, s);
+  return launch_kv_merge(a, line, ctas, kRowsT, ctas > 8 * items, kLift, s);
 }
 
 }  // namespace
@@ -747,10 +758,11 @@ size_t kv_attn_workspace(int sms, int d) {
   return 256 + (size_t)3 * sms * (sizeof(KvOpen) + 2 * kv_part_floats(kRowsT, d) * sizeof(float));
 }
 
-cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, int split, float lift,
+cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, bool many, float lift,
                             cudaStream_t s) {
+  const int per_row = many ? kMergeWarps : 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3((unsigned)ctas, (unsigned)split);
+  cfg.gridDim = dim3((unsigned)ctas, (unsigned)(rows * per_row / kMergeWarps));
   cfg.blockDim = dim3(32 * kMergeWarps);
   cfg.stream = s;
   cudaLaunchAttribute at[1];
@@ -759,10 +771,10 @@ cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, i
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (a.c.d == 128)
-    return a.is_bf16 ? cudaLaunchKernelEx(&cfg, kv_merge_kernel<128, true>, a, line, rows, lift)
-                     : cudaLaunchKernelEx(&cfg, kv_merge_kernel<128, false>, a, line, rows, lift);
-  return a.is_bf16 ? cudaLaunchKernelEx(&cfg, kv_merge_kernel<64, true>, a, line, rows, lift)
-                   : cudaLaunchKernelEx(&cfg, kv_merge_kernel<64, false>, a, line, rows, lift);
+    return a.is_bf16 ? cudaLaunchKernelEx(&cfg, kv_merge_kernel<128, true>, a, line, rows, lift, per_row)
+                     : cudaLaunchKernelEx(&cfg, kv_merge_kernel<128, false>, a, line, rows, lift, per_row);
+  return a.is_bf16 ? cudaLaunchKernelEx(&cfg, kv_merge_kernel<64, true>, a, line, rows, lift, per_row)
+                   : cudaLaunchKernelEx(&cfg, kv_merge_kernel<64, false>, a, line, rows, lift, per_row);
 }
 
 cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, const int* gate, cudaStream_t s) {

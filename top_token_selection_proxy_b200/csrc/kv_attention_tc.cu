@@ -722,8 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (tid == 0 && !all && w.t0 == 0)
-          args.line.open[blockIdx.x] = {w.at + it.tiles, w.total, it.row0, (int)blockIdx.x, (int)w.ctas,
-                                        it.h * a.group, it.rr0, it.valid, 1};
+          args.line.open[blockIdx.x] = {it.row0, (int)blockIdx.x, it.h * a.group, it.rr0, it.valid,
+                                        kv_parts(w.at + it.tiles, w.total, w.ctas) - (int)blockIdx.x};
       }
       n += nt;
     }
@@ -761,7 +761,7 @@ cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, cons
   if (e != cudaSuccess) return e;
   kv_attn_tc_kernel<<<sms, kThreads, kSmem, s>>>(kmap, vmap, t);
   e = cudaGetLastError();
-  if (e == cudaSuccess) e = launch_kv_merge(a, t.line, sms, M, 16, kLift, s);
+  if (e == cudaSuccess) e = launch_kv_merge(a, t.line, sms, M, sms > 8 * (a.st.B + a.st.rows * a.group / M) * (int64_t)a.c.hk, kLift, s);
   if (e != cudaSuccess) return e;
   return launch_kv_attn(a, sms, p + 256 + (size_t)sms * (sizeof(KvOpen) + 2 * kv_part_floats(M, D) * sizeof(float)),
                         t.gate, s);
