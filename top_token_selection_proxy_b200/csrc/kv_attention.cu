@@ -16,6 +16,8 @@
 // Work is cut evenly whatever the lengths are: all tiles of 128 tokens of all (sequence, key head, 16 query rows)
 // stand in one line, and every CTA takes an equal stretch of it.  A stretch that begins or ends inside an item
 // leaves a partial result, which kv_merge_kernel joins in a fixed order.
+#include <type_traits>
+
 #include "kv.cuh"
 
 namespace pivot {
@@ -86,7 +88,7 @@ struct Shape {
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kKPieces = 4 * (D / 64);         // 16-byte pieces of keys a lane holds of 32 tokens
   static constexpr int kVBytes = D / 8;                 // bytes of a value a lane holds
-  static constexpr int kStageBytes = 32 * (kKPieces * 16 + 8 * kVBytes);  // a warp's
+  static constexpr int kStageBytes = 32 * (kKPieces * 16 + 8 * kVBytes + 4);  // a warp's; 4: the tokens' scales
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQParts = BF16 ? 1 : 3;
   static constexpr int kQBytes = BF16 ? 0 : kQParts * (D / 16) * 32 * 16;
@@ -108,13 +110,17 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   }
 
   // this CTA's stretch of the line
-  int64_t total = 0, sel_rows = 0;
+  int64_t total = 0, sel_rows = 0, w_first = 0;  // w_first: of the lane's first sequence
   const int sel_rt = (a.group + kRowsT - 1) / kRowsT, sel_tiles = (a.topk + kTile - 1) / kTile;
   if (SEL) {
     sel_rows = max64(min64(a.st.off[a.st.B], a.st.rows), 0);
     total = sel_rows * a.c.hk * sel_rt * sel_tiles;
   } else {
-    for (int b = lane; b < a.st.B; b += 32) total += weight_of(a, b);
+    for (int b = lane; b < a.st.B; b += 32) {
+      const int64_t w = weight_of(a, b);
+      if (b < 32) w_first = w;
+      total += w;
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
   }
@@ -142,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
     int64_t run = 0;
     for (int b0 = 0;; b0 += 32) {
       if (b0 >= a.st.B) return;  // only where the lengths changed under the call
-      const int64_t w = weight_of(a, b0 + lane);
+      const int64_t w = b0 ? weight_of(a, b0 + lane) : w_first;
       int64_t inc = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -294,58 +300,58 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       if (s < 0 || s > hi) return -1;
       return kv_page(a.st, a.c, b, (uint32_t)s);
     };
-    // the copies of one step; returns the lane's token's scales: ke + 127 in the low byte, ve as bf16 in the upper
-    // half; 0 where it is absent
-    auto issue = [&](int step, int s, int page) -> uint32_t {
-      uint32_t ex = 0;
-      if (step < steps) {
-        const uint32_t dst = ring + (step % kStages) * S::kStageBytes + lane * 16;
-        const uint32_t in = page >= 0 ? (uint32_t)s % (uint32_t)a.c.ps : 0u;
-        const int slot = page >= 0 ? (page * a.c.hk + h) * a.c.ps + (int)in : -1;  // row of the cache
-        if (page >= 0) {
-          const int64_t be = ((int64_t)page * a.c.hk + h) * (a.c.ps / kKvBlock) + in / kKvBlock;
-          ex = (uint32_t)(max((int)__ldg(a.c.ke + be), -126) + 127) | __float_as_uint((float)__ldg(a.c.ve + be));
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int sl = __shfl_sync(~0u, slot, 8 * j + g);
-          const uint8_t* src = a.c.k + (int64_t)max(sl, 0) * D + 16 * tig;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-            cp_async_or_zero<16>(dst + (j * (D / 64) + c) * 512, src + 64 * c, sl >= 0);
-        }
-        const uint32_t vdst = ring + (step % kStages) * S::kStageBytes + S::kKPieces * 512 + lane * S::kVBytes;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int sl = __shfl_sync(~0u, slot, 16 * (j / 4) + 8 * (j / 2 % 2) + 2 * tig + j % 2);
-          cp_async_or_zero<S::kVBytes>(vdst + j * 32 * S::kVBytes, a.c.v + (int64_t)max(sl, 0) * D + S::kVBytes * g,
-                                       sl >= 0);
-        }
+    // The copies of one step, and the loads of the lane's token's scales.  They are kept beside the copies: ke + 127 in
+    // the low byte, ve as bf16 in the upper half; 0 where the token is absent.
+    int pend_ke = 0, pend_ve = 0;
+    uint32_t pend_at = 0;
+    auto issue = [&](int step, int s, int page) {
+      const uint32_t at_stage = (step % kStages) * S::kStageBytes;
+      const uint32_t dst = ring + at_stage + lane * 16;
+      uint32_t in = 0;
+      int slot = -1;  // row of the cache
+      pend_at = at_stage;
+      pend_ke = pend_ve = 0;
+      if (page >= 0) {
+        in = (uint32_t)s % (uint32_t)a.c.ps;
+        const int ph = page * a.c.hk + h;
+        slot = ph * a.c.ps + (int)in;
+        const int64_t be = (int64_t)ph * (a.c.ps / kKvBlock) + in / kKvBlock;
+        pend_ke = 0x100 | (uint8_t)__ldg(a.c.ke + be);  // not waited for here
+        pend_ve = __ldg(a.c.ve + be);
       }
-      cp_async_commit();
-      return ex;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int sl = __shfl_sync(~0u, slot, 8 * j + g);
+        const uint8_t* src = a.c.k + ((int64_t)max(sl, 0) * D + 16 * tig);
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+          cp_async_or_zero<16>(dst + (j * (D / 64) + c) * 512, src + 64 * c, sl >= 0);
+      }
+      const uint32_t vdst = ring + at_stage + S::kKPieces * 512 + lane * S::kVBytes;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int sl = __shfl_sync(~0u, slot, 16 * (j / 4) + 8 * (j / 2 % 2) + 2 * tig + j % 2);
+        cp_async_or_zero<S::kVBytes>(vdst + j * 32 * S::kVBytes, a.c.v + ((int64_t)max(sl, 0) * D + S::kVBytes * g), sl >= 0);
+      }
+    };
+    // The scales of the copies issued last, one step later.
+    auto settle = [&]() {
+      const uint32_t ex = pend_ke ? (uint32_t)(max((int)(int8_t)pend_ke, -126) + 127) | __float_as_uint((float)pend_ve) : 0u;
+      *reinterpret_cast<uint32_t*>(smem + (ring - smem_u32(smem)) + pend_at + S::kKPieces * 512 + 256 * S::kVBytes + lane * 4) = ex;
     };
 
-    uint32_t exps[kStages];  // of the steps in flight, the next one first
-    int s_next, page_next, s_after;
-    {
-      int s[kStages + 1], pg[kStages + 1];
-#pragma unroll
-      for (int i = 0; i <= kStages; ++i) s[i] = load_entry(i);
-#pragma unroll
-      for (int i = 0; i <= kStages; ++i) pg[i] = load_page(s[i]);
-#pragma unroll
-      for (int i = 0; i < kStages; ++i) exps[i] = issue(i, s[i], pg[i]);
-      s_next = s[kStages];
-      page_next = pg[kStages];
-      s_after = load_entry(kStages + 1);
-    }
-
-    for (int step = 0; step < steps; ++step) {
-      const uint32_t ex = exps[0];
-      cp_async_wait<kStages - 1>();  // a lane reads only what it copied itself
+    // One loop for both ends: step + kStages is copied after step was computed, and the first kStages before any was.
+    // (Its code is read once; a CTA's first pass through new code costs more than its work.)
+    int s_next = load_entry(0), s_after = load_entry(1);
+    int page_next = load_page(s_next);
+#pragma unroll 1
+    for (int step = -kStages; step < steps; ++step) {
+     if (step >= 0) {
+      cp_async_wait<kStages - 1>();  // a lane reads only what it copied itself; the scales are the warp's
+      __syncwarp();
       const uint8_t* const kst = smem + (ring - smem_u32(smem)) + (step % kStages) * S::kStageBytes;
       const uint8_t* const vst = kst + S::kKPieces * 512;
+      const uint32_t* const scales = reinterpret_cast<const uint32_t*>(vst + 256 * S::kVBytes);
       const int base = base_of(step);
 
       // scores: 4 tiles of 8 tokens
@@ -385,20 +391,19 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       // scale, mask
       float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
       uint32_t te[4][2];  // scales of the two tokens that this lane holds in each tile
-      const bool whole = __all_sync(~0u, ex != 0) &&
+      const bool whole = __all_sync(~0u, scales[lane] != 0) &&
                          (SEL || (base + kWTok - 1 <= min64(p_lo, hi) &&
                                   (a.window <= 0 || base > p_hi - a.window || base + kWTok <= a.sinks)));
       if (SEL) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-          for (int k = 0; k < 2; ++k) te[j][k] = __shfl_sync(~0u, ex, 8 * j + 2 * tig + k);
+        for (int j = 0; j < 4; ++j) {
+          const uint2 w = *reinterpret_cast<const uint2*>(scales + 8 * j + 2 * tig);
+          te[j][0] = w.x, te[j][1] = w.y;
+        }
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; j += 2) {  // a block's tokens share one
-          const uint32_t w = __shfl_sync(~0u, ex, 8 * j);
-          te[j][0] = te[j][1] = te[j + 1][0] = te[j + 1][1] = w;
-        }
+        for (int j = 0; j < 4; j += 2)  // a block's tokens share one
+          te[j][0] = te[j][1] = te[j + 1][0] = te[j + 1][1] = scales[8 * j];
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
@@ -520,14 +525,13 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
         }
         odd = __any_sync(~0u, odd);
       }
-#pragma unroll 1
-      for (int only = odd ? 0 : -1; only < (odd ? valid : 0); ++only) {
+      auto product = [&](auto by_row, int only) {  // by_row: of row `only` alone
         const int64_t p = first + (rr0 + max(only, 0)) / a.group;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t w[4][VW];
           value(u, w);
-          if (odd) {
+          if (by_row) {
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int s = base + 16 * u + 8 * (j / 2) + 2 * tig + j % 2;
@@ -545,25 +549,33 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
             const uint32_t b1[4] = {cvt_e4m3x2(l1), cvt_e4m3x2(l1 >> 16), cvt_e4m3x2(h1), cvt_e4m3x2(h1 >> 16)};
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4) {
-              if (BF16 && !odd) {
+              if (BF16 && !by_row) {
                 mma16816(o[4 * k + q4], pa[u], b0[q4], b1[q4]);
-              } else {  // fp32: a block's own sum first, then one addition; odd: of one row alone
+              } else {  // fp32: a block's own sum first, then one addition
                 float t4[4] = {0.f, 0.f, 0.f, 0.f};
                 if (!BF16) mma16816(t4, pb[u], b0[q4], b1[q4]);
                 mma16816(t4, pa[u], b0[q4], b1[q4]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                  if (!odd || only == g + 8 * (i / 2)) o[4 * k + q4][i] += t4[i];
+                  if (!by_row || only == g + 8 * (i / 2)) o[4 * k + q4][i] += t4[i];
               }
             }
           }
         }
+      };
+      if (!odd) {
+        product(std::false_type{}, -1);
+      } else {
+#pragma unroll 1
+        for (int only = 0; only < valid; ++only) product(std::true_type{}, only);
       }
+     }
 
-      // the next copies go where this step's were; every lane is past its own reads
-#pragma unroll
-      for (int i = 0; i + 1 < kStages; ++i) exps[i] = exps[i + 1];
-      exps[kStages - 1] = issue(step + kStages, s_next, page_next);
+      // the next copies go where this step's were; every lane is past its own reads, and the warp past the scales
+      __syncwarp();
+      if (step > -kStages) settle();
+      if (step + kStages < steps) issue(step + kStages, s_next, page_next);
+      cp_async_commit();
       page_next = load_page(s_after);
       s_next = s_after;
       s_after = load_entry(step + kStages + 2);
