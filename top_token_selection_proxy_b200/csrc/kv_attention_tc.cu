@@ -8,8 +8,9 @@
 //               (scaled to 2^8; what lies 2^-10 below a row's largest keeps fewer), two products into one sum.
 //   O += P V    kind::f16.  Weights leave the softmax as fp16 and stay in tensor memory, where S was; four warps
 //               turn the values into fp16.
-// Two tiles are in work at a time, each with its own S, O and softmax warpgroup: while one is in the softmax, the
-// tensor core multiplies for the other.  Both results are joined at the item's end.
+// Two tiles are in work at a time, each with its own S, P and softmax warpgroup, into one O: while one is in the
+// softmax, the tensor core multiplies for the other, and a tile's scores are there before its warpgroup has finished
+// the weights of the tile before.  The rows' reference m' passes from tile to tile in shared memory.
 //
 // What bounds it: the exponentials (16 a clock and SM: 1024 clocks a tile) and the products (1024 clocks) for full
 // items; with half the rows or fewer the cache's bytes.
@@ -217,13 +218,14 @@ struct Walk {
 };
 
 struct Tail {
-  uint64_t kf[kKS], ke[kKS], vf[kVS], ve[kVS], hf[2], he[2], sf[2], pf[2], mf[kMeta], qf, of, xf;
+  uint64_t kf[kKS], ke[kKS], vf[kVS], ve[kVS], hf[2], he[2], sf[2], sc[2], pf[2], rf[2], od[2], mf[kMeta], qf, of, xf;
   uint32_t tmem_slot;
   volatile int abort_flag;
   Meta meta[kMeta];
   Walk walk[kWMma + 1];  // one for each warp: in registers it would crowd out the softmax
   float unit[M];
-  float stats[2][M][3];
+  float ref[M];          // m' of each row
+  float stats[2][M][2];  // (m, l) of each half's tiles
 };
 
 constexpr int kOffQ = 0, kOffK = 2 * M * D, kOffV = kOffK + kKS * kTileB, kOffH = kOffV + kVS * kTileB,
@@ -273,7 +275,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kVS; ++i) mbar_init(&T.vf[i], 1), mbar_init(&T.ve[i], kConv);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&T.hf[i], kConv), mbar_init(&T.he[i], 1);
-      mbar_init(&T.sf[i], 1), mbar_init(&T.pf[i], kSoft / 2);
+      mbar_init(&T.sf[i], 1), mbar_init(&T.sc[i], kSoft / 2), mbar_init(&T.pf[i], kSoft / 2);
+      mbar_init(&T.rf[i], kSoft / 2), mbar_init(&T.od[i], 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&T.mf[i], 1);
     mbar_init(&T.qf, kSoft);
@@ -290,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = T.tmem_slot;  // S0, S1, O0, O1: 128 columns each
+  const uint32_t tmem = T.tmem_slot;  // 128 columns each of S0, S1 and O, 64 each of P0, P1
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     if (mbar_wait(bar, parity, args.timeout_ns, &T.abort_flag)) return true;
     T.abort_flag = 1;
@@ -389,35 +392,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == kWMma) {
     // ------------------------------------------------------------ products (one thread)
-    uint32_t n = 0, items = 0, seen[2] = {0, 0};  // tiles; items; weights taken, of each half
+    uint32_t n = 0, items = 0, before[2] = {0, 0};  // tiles, items; tiles of each half before this item
     bool ok = true;
     for (; w.live && ok; advance(), ++items) {
       const int nt = w.t1 - w.t0;
       if (lane == 0) {
         const uint32_t qaddr = smem_u32(smem + kOffQ);
-        auto second = [&](int k) {  // O += P V of the item's tile k
-          const uint32_t i = n - (uint32_t)(nt - k);  // n: tiles up to this item's end
-          const int s = k & 1, hb = i & 1;
-          if (!wait(&T.pf[s], seen[s]++ & 1) || !wait(&T.hf[hb], i / 2 & 1)) return false;
-          tc_fence_after();
-          const uint32_t v = smem_u32(smem + kOffH) + hb * (kTok * D * 2);
-#pragma unroll
-          for (int kk = 0; kk < kTok / 16; ++kk)
-            umma_f16_ts(tmem + 256 + 128 * s, tmem + 128 * s + 8 * kk,
-                        sw128_mnmajor_desc(v + kk * 16 * 128, kTok * 128, 1024), idesc_f16_f32_bmn(M, D),
-                        k >= 2 || kk > 0);
-          umma_commit(&T.he[hb]);
-          return true;
-        };
-        const uint32_t n0 = n;
-        n += nt;
-        ok = wait(&T.qf, items & 1);
-        tc_fence_after();
-        for (int k = 0; k < nt && ok; ++k) {
-          const uint32_t i = n0 + k;
+        auto scores = [&](int k) {  // S = Q K^T of the item's tile k, once its half's last S has been read
+          const uint32_t i = n + k;
           const int ks = i % kKS, s = k & 1;
-          ok = wait(&T.kf[ks], i / kKS & 1);
-          if (!ok) break;
+          if (k >= 2 && !wait(&T.sc[s], (before[s] + (k - 2) / 2) & 1)) return false;
+          if (!wait(&T.kf[ks], i / kKS & 1)) return false;
           tc_fence_after();
           const uint32_t kaddr = smem_u32(smem + kOffK) + ks * kTileB;
 #pragma unroll
@@ -428,10 +413,30 @@ __global__ void __launch_bounds__(kThreads, 1)
                       sw128_kmajor_desc(kaddr + kk * 32), idesc_e4m3_f32(M, kTok), part == 0 || kk > 0);
           umma_commit(&T.ke[ks]);
           umma_commit(&T.sf[s]);
-          if (k > 0) ok = second(k - 1);
-        }
-        if (ok) ok = second(nt - 1);
+          return true;
+        };
+        auto sums = [&](int k) {  // O += P V
+          const uint32_t i = n + k;
+          const int s = k & 1, hb = i & 1;
+          if (!wait(&T.pf[s], (before[s] + k / 2) & 1) || !wait(&T.hf[hb], i / 2 & 1)) return false;
+          tc_fence_after();
+          const uint32_t v = smem_u32(smem + kOffH) + hb * (kTok * D * 2);
+#pragma unroll
+          for (int kk = 0; kk < kTok / 16; ++kk)
+            umma_f16_ts(tmem + 256, tmem + 384 + 64 * s + 8 * kk,
+                        sw128_mnmajor_desc(v + kk * 16 * 128, kTok * 128, 1024), idesc_f16_f32_bmn(M, D), k > 0 || kk > 0);
+          umma_commit(&T.he[hb]);
+          umma_commit(&T.od[s]);
+          return true;
+        };
+        ok = wait(&T.qf, items & 1);
+        tc_fence_after();
+        if (ok) ok = scores(0) && (nt == 1 || scores(1));
+        for (int k = 0; k < nt && ok; ++k) ok = (k + 2 >= nt || scores(k + 2)) && sums(k);
         if (ok) umma_commit(&T.of);
+        n += nt;
+        before[0] += (nt + 1) / 2;
+        before[1] += nt / 2;
       }
       ok = __shfl_sync(~0u, (int)ok, 0);
     }
@@ -481,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------ softmax: a thread for a row, a warpgroup for a half
     const int s = warp / 4, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // lane 32 * (warp % 4) in an address' upper half
-    const uint32_t sc = tmem + lanes + 128 * s, oc = tmem + lanes + 256 + 128 * s;
-    uint32_t n = 0, items = 0, mine = 0;  // tiles of both halves; items; tiles of this half
+    const uint32_t sc = tmem + lanes + 128 * s, oc = tmem + lanes + 256, pc = tmem + lanes + 384 + 64 * s;
+    uint32_t n = 0, items = 0, mine = 0, theirs = 0;  // tiles of both halves; items; tiles of this half, of the other before this item
     bool ok = true;
     // after a failed wait the loop only keeps the barriers' count
     for (; w.live; advance(), ++items) {
@@ -545,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(~0u, ok && wait(&T.qf, items & 1));
       const float unit = T.unit[r];
       const bool idle = 32 * (warp % 4) >= it.valid;  // a warp without rows
-      float m = -INFINITY, mp = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;
       for (int k = s; k < nt; k += 2, ++mine) {
         const uint32_t i = n + k;
         const int base = it.tile(w.t0 + k) * kTok;
@@ -553,110 +558,123 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = __all_sync(~0u, wait(&T.mf[i % kMeta], i / kMeta & 1) && wait(&T.sf[s], mine & 1));
         if (!ok) continue;
         tc_fence_after();
-        if (!idle) {
-          const Meta& me = T.meta[i % kMeta];
-          const uint32_t present = me.present;
-          const bool whole = present == 0xFFu && whole_tile(a, it, base);
-          // which of 32 columns this row sees, where the tile is not whole
-          const int upto = (int)max64(min64(min64(it.hi, pos) - base + 1, kTok), 0);
-          const int from = a.window > 0 ? (int)max64(min64(pos - a.window + 1 - base, kTok), 0) : 0;
-          const int sinks = a.window > 0 ? (int)max64(min64(a.sinks - base, kTok), 0) : 0;
-          auto seen = [&](int c) {
+        const Meta& me = T.meta[i % kMeta];
+        const uint32_t present = me.present;
+        const bool whole = present == 0xFFu && whole_tile(a, it, base);
+        // which of 32 columns this row sees, where the tile is not whole
+        const int upto = (int)max64(min64(min64(it.hi, pos) - base + 1, kTok), 0);
+        const int from = a.window > 0 ? (int)max64(min64(pos - a.window + 1 - base, kTok), 0) : 0;
+        const int sinks = a.window > 0 ? (int)max64(min64(a.sinks - base, kTok), 0) : 0;
+        auto load = [&](int c, auto all, uint32_t (&x)[32]) {  // 32 scores; hidden ones -inf
+          tmem_ld32x32b_x32(sc + 32 * c, x);
+          tmem_wait_ld();
+          if (!all) {
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
             const uint32_t there = ((present >> (2 * c) & 1) ? 0xFFFFu : 0u) | ((present >> (2 * c + 1) & 1) ? 0xFFFF0000u : 0u);
-            return below(upto - 32 * c) & (~below(from - 32 * c) | below(sinks - 32 * c)) & there;
-          };
-          // One pass over S, 32 columns at a time.  The weights' reference m' (and m, the sum's) may lag behind the
-          // largest score by 2^13; where it would by more, what was weighed with the old one is scaled down: the
-          // output sums, and this tile's weights so far.  After the first columns of an item that is rare.
-          // The loop is not unrolled: its code then stays in the instruction cache (unrolled it ran at half the speed).
-          float mpr = mp == -INFINITY ? 0.f : mp;
-          float back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));  // product's weights to the sum's, but for 2^-ve
-          auto weigh = [&](auto all) {  // two copies: as one, the compiler masks every tile
+            const uint32_t see = below(upto - 32 * c) & (~below(from - 32 * c) | below(sinks - 32 * c)) & there;
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              if (!(see >> j & 1)) x[j] = 0xFF800000u;
+          }
+        };
+        // what a block's scores are multiplied by; never 0: a hidden score, -inf, times it stays -inf
+        auto factor = [&](float ks) { return fmaxf(unit * ks, 1e-37f); };
+        // The loops are not unrolled, and masked tiles have code of their own: the code then stays in the instruction
+        // cache (unrolled it ran at half the speed; in one copy the compiler masks every tile).
+        float top = -INFINITY, topv = -INFINITY;
+        auto largest = [&](auto all) {
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t x[32];
-              tmem_ld32x32b_x32(sc + 32 * c, x);
-              const float2 ks = *reinterpret_cast<const float2*>(&me.ks[2 * c]), ve = *reinterpret_cast<const float2*>(&me.ve[2 * c]),
-                           iv = *reinterpret_cast<const float2*>(&me.iv[2 * c]);
-              // never 0: a hidden score, -inf, times it stays -inf
-              const float cb[2] = {fmaxf(unit * ks.x, 1e-37f), fmaxf(unit * ks.y, 1e-37f)};
-              tmem_wait_ld();
-              if (!all) {
-                const uint32_t see = seen(c);
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32];
+            load(c, all, x);
+            float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-                for (int j = 0; j < 32; ++j)
-                  if (!(see >> j & 1)) x[j] = 0xFF800000u;
-              }
-              float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) {
-                t0 = fmaxf(t0, __uint_as_float(x[j]));
-                t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
-              }
-              t0 *= cb[0];
-              t1 *= cb[1];
-              const float top = fmaxf(t0, t1), topv = fmaxf(t0 + ve.x, t1 + ve.y);
-              const bool up = topv > mp + kSlack, up_sum = top > m + kSlack;
-              if (__any_sync(~0u, up || up_sum)) {
-                if (up_sum) {
-                  l *= m == -INFINITY ? 1.f : ex2(m - top);
-                  m = top;
-                }
-                const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
-                if (up) mp = topv;
-                mpr = mp == -INFINITY ? 0.f : mp;
-                back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));
-                if (__any_sync(~0u, f != 1.f)) {
-                  uint32_t y[16];
-                  if (k >= 2) {
-#pragma unroll 1
-                    for (int q = 0; q < D / 16; ++q) {
-                      tmem_ld32x32b_x16(oc + 16 * q, y);
-                      tmem_wait_ld();
-#pragma unroll
-                      for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-                      tmem_st32x32b_x16(oc + 16 * q, y);
-                    }
-                  }
-                  tmem_wait_st();
-                  const __half2 fh = __float2half2_rn(f);
-#pragma unroll 1
-                  for (int q = 0; q < c; ++q) {
-                    tmem_ld32x32b_x16(sc + 16 * q, y);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 16; ++j) {
-                      const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[j]), fh);
-                      y[j] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    tmem_st32x32b_x16(sc + 16 * q, y);
-                  }
-                  tmem_wait_st();
-                }
-              }
-              uint32_t y[16];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float off = (u ? ve.y : ve.x) - mpr + kLift;
-                const uint64_t off2 = two(off, off), cb2 = two(cb[u], cb[u]);
-                uint64_t sum = two(0.f, 0.f);
-#pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                  float d0, d1;
-                  split(fma2(two(__uint_as_float(x[16 * u + j]), __uint_as_float(x[16 * u + j + 1])), cb2, off2), d0, d1);
-                  d0 = ex2(d0);
-                  d1 = ex2(d1);
-                  sum = add2(sum, two(d0, d1));
-                  y[8 * u + j / 2] = pack_f16(d0, d1);
-                }
-                float s0, s1;
-                split(sum, s0, s1);
-                l = fmaf(s0 + s1, back * (u ? iv.y : iv.x), l);
-              }
-              tmem_st32x32b_x16(sc + 16 * c, y);
+            for (int j = 0; j < 16; ++j) {
+              t0 = fmaxf(t0, __uint_as_float(x[j]));
+              t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
             }
-          };
+            t0 *= factor(me.ks[2 * c]);
+            t1 *= factor(me.ks[2 * c + 1]);
+            top = fmaxf(top, fmaxf(t0, t1));
+            topv = fmaxf(topv, fmaxf(t0 + me.ve[2 * c], t1 + me.ve[2 * c + 1]));
+          }
+        };
+        if (!idle) {
+          if (whole) largest(std::true_type{});
+          else largest(std::false_type{});
+        }
+        // The weights' reference m' (and m, the sum's) may lag behind the largest score by 2^13; where it would by
+        // more, the output sums so far are scaled down, after the tile before has gone into them.  After the first
+        // tiles of an item that is rare.
+        if (k > 0) {
+          ok = __all_sync(~0u, wait(&T.rf[s ^ 1], (theirs + (k - 1) / 2) & 1));
+          if (!ok) continue;
+        }
+        float mp = k > 0 ? T.ref[r] : -INFINITY;
+        const bool up = topv > mp + kSlack;
+        const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
+        if (up) mp = topv;
+        T.ref[r] = mp;
+        mbar_arrive(&T.rf[s]);
+        if (__any_sync(~0u, f != 1.f)) {
+          ok = __all_sync(~0u, wait(&T.od[s ^ 1], (theirs + (k - 1) / 2) & 1));
+          if (!ok) continue;
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t y[16];
+            tmem_ld32x32b_x16(oc + 16 * q, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
+            tmem_st32x32b_x16(oc + 16 * q, y);
+          }
+        }
+        if (top > m + kSlack) {
+          l *= m == -INFINITY ? 1.f : ex2(m - top);
+          m = top;
+        }
+        const float mpr = mp == -INFINITY ? 0.f : mp;
+        const float back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));  // product's weights to the sum's, but for 2^-ve
+        if (k >= 2) {  // this half's weights of two tiles ago have been multiplied
+          ok = __all_sync(~0u, wait(&T.od[s], (mine - 1) & 1));
+          if (!ok) continue;
+          tc_fence_after();
+        }
+        auto weigh = [&](auto all) {
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], y[16];
+            load(c, all, x);
+            if (c == 3) {  // S may be overwritten
+              tc_fence_before();
+              mbar_arrive(&T.sc[s]);
+            }
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float cb = factor(me.ks[2 * c + u]), off = me.ve[2 * c + u] - mpr + kLift;
+              const uint64_t off2 = two(off, off), cb2 = two(cb, cb);
+              uint64_t sum = two(0.f, 0.f);
+#pragma unroll
+              for (int j = 0; j < 16; j += 2) {
+                float d0, d1;
+                split(fma2(two(__uint_as_float(x[16 * u + j]), __uint_as_float(x[16 * u + j + 1])), cb2, off2), d0, d1);
+                d0 = ex2(d0);
+                d1 = ex2(d1);
+                sum = add2(sum, two(d0, d1));
+                y[8 * u + j / 2] = pack_f16(d0, d1);
+              }
+              float s0, s1;
+              split(sum, s0, s1);
+              l = fmaf(s0 + s1, back * me.iv[2 * c + u], l);
+            }
+            tmem_st32x32b_x16(pc + 16 * c, y);
+          }
+        };
+        if (idle) {
+          tc_fence_before();
+          mbar_arrive(&T.sc[s]);
+        } else {
           if (whole) weigh(std::true_type{});
           else weigh(std::false_type{});
           tmem_wait_st();
@@ -664,29 +682,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         mbar_arrive(&T.pf[s]);
       }
-      // both halves together: each warpgroup takes half of the dims
+      theirs += s == 0 ? nt / 2 : (nt + 1) / 2;
+      // the item's sums: each warpgroup takes half of the dims
       ok = __all_sync(~0u, ok && wait(&T.of, items & 1));
       tc_fence_after();
-      T.stats[s][r][0] = mp;
-      T.stats[s][r][1] = m;
-      T.stats[s][r][2] = l;
+      T.stats[s][r][0] = m;
+      T.stats[s][r][1] = l;
       mbar_arrive(&T.xf);
       ok = __all_sync(~0u, ok && wait(&T.xf, items & 1));
       if (ok && !idle) {
-        float mps[2], ms[2], ls[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) mps[u] = T.stats[u][r][0], ms[u] = T.stats[u][r][1], ls[u] = T.stats[u][r][2];
-        const float mpt = fmaxf(mps[0], mps[1]), mt = fmaxf(ms[0], ms[1]);
-        float lt = 0.f, f[2];
-        bool use[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          use[u] = !(mps[u] == -INFINITY && ls[u] == 0.f) && u < nt;
-          f[u] = mps[u] == -INFINITY ? 1.f : ex2(mps[u] - mpt);
-          lt += ms[u] == -INFINITY ? ls[u] : ls[u] * ex2(ms[u] - mt);
-        }
+        const float mpt = T.ref[r], m0 = T.stats[0][r][0], m1 = T.stats[1][r][0], l0 = T.stats[0][r][1], l1 = T.stats[1][r][1];
+        const float mt = fmaxf(m0, m1);
+        const float lt = (m0 == -INFINITY ? l0 : l0 * ex2(m0 - mt)) + (m1 == -INFINITY ? l1 : l1 * ex2(m1 - mt));
+        const bool none = mpt == -INFINITY && lt == 0.f;  // the row saw nothing
         const bool all = w.t0 == 0 && w.t1 == it.tiles;
-        const float g = all ? (lt == 0.f ? 0.f : ex2(mpt - mt - kLift) / lt) : 1.f;
+        const float g = all && !none ? ex2(mpt - mt - kLift) / lt : 1.f;
         const int rr = it.rr0 + r;
         const int64_t row = it.row0 + rr / a.group;
         const int j = it.h * a.group + rr % a.group;
@@ -695,20 +705,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < 2; ++c) {
           const int d0 = 64 * s + 32 * c;
-          uint32_t x[32], y[32];
-          tmem_ld32x32b_x32(tmem + lanes + 256 + d0, x);
-          if (nt > 1) tmem_ld32x32b_x32(tmem + lanes + 384 + d0, y);
+          uint32_t x[32];
+          tmem_ld32x32b_x32(oc + d0, x);
           tmem_wait_ld();
           if (put) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               float v[4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                v[q] = use[0] ? __uint_as_float(x[e + q]) * f[0] : 0.f;
-                if (use[1]) v[q] += __uint_as_float(y[e + q]) * f[1];
-                v[q] *= g;
-              }
+              for (int q = 0; q < 4; ++q) v[q] = none ? 0.f : __uint_as_float(x[e + q]) * g;
               if (all) kv_store4(a, (row * a.hq + j) * (int64_t)D + d0 + e, v[0], v[1], v[2], v[3], true);
               else *reinterpret_cast<float4*>(part + r * D + d0 + e) = make_float4(v[0], v[1], v[2], v[3]);
             }
