@@ -25,8 +25,8 @@ constexpr int D = 128, M = 128, kTok = 128;
 constexpr int kKS = 4, kVS = 3, kMeta = 8;   // stages of keys, of raw values, of the blocks' scales
 constexpr int kTileB = kTok * D;             // bytes of an e4m3 tile
 constexpr int kSoft = 256, kConv = 128;      // threads: two softmax warpgroups, one of the converters
-constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWMma = kWTma + 1;
-constexpr int kThreads = 32 * (kWMma + 1);
+constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWQk = kWTma + 1, kWPv = kWQk + 1;
+constexpr int kThreads = 32 * (kWPv + 1);
 constexpr float kLift = 2.f, kSlack = 13.f;  // weights up to 2^15: the maxima may lag by 2^13 before sums are rescaled
 
 struct Meta {  // of a tile's 8 blocks
@@ -222,7 +222,7 @@ struct Tail {
   uint32_t tmem_slot;
   volatile int abort_flag;
   Meta meta[kMeta];
-  Walk walk[kWMma + 1];  // one for each warp: in registers it would crowd out the softmax
+  Walk walk[kWPv + 1];  // one for each warp: in registers it would crowd out the softmax
   float unit[M];
   float ref[M];          // m' of each row
   float stats[2][M][2];  // (m, l) of each half's tiles
@@ -286,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     args.line.open[blockIdx.x].open = 0;
   }
-  if (warp == kWMma) {
+  if (warp == kWQk) {
     tmem_alloc(&T.tmem_slot, 512);
     tmem_relinquish();
   }
@@ -390,19 +390,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
-  } else if (warp == kWMma) {
-    // ------------------------------------------------------------ products (one thread)
+  } else if (warp == kWQk || warp == kWPv) {
+    // ------------------------------------------------------------ products (one thread of each of two warps, so that
+    // one's waits do not keep the other's products back)
     uint32_t n = 0, items = 0, before[2] = {0, 0};  // tiles, items; tiles of each half before this item
     bool ok = true;
     for (; w.live && ok; advance(), ++items) {
       const int nt = w.t1 - w.t0;
-      if (lane == 0) {
+      if (lane == 0 && warp == kWQk) {
         const uint32_t qaddr = smem_u32(smem + kOffQ);
-        auto scores = [&](int k) {  // S = Q K^T of the item's tile k, once its half's last S has been read
+        ok = wait(&T.qf, items & 1);
+        for (int k = 0; k < nt && ok; ++k) {  // S = Q K^T, once the half's last S has been read
           const uint32_t i = n + k;
           const int ks = i % kKS, s = k & 1;
-          if (k >= 2 && !wait(&T.sc[s], (before[s] + (k - 2) / 2) & 1)) return false;
-          if (!wait(&T.kf[ks], i / kKS & 1)) return false;
+          ok = (k < 2 || wait(&T.sc[s], (before[s] + (k - 2) / 2) & 1)) && wait(&T.kf[ks], i / kKS & 1);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t kaddr = smem_u32(smem + kOffK) + ks * kTileB;
 #pragma unroll
@@ -411,33 +413,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int kk = 0; kk < D / 32; ++kk)
               umma_f8(tmem + 128 * s, sw128_kmajor_desc(qaddr + part * M * D + kk * 32),
                       sw128_kmajor_desc(kaddr + kk * 32), idesc_e4m3_f32(M, kTok), part == 0 || kk > 0);
-          umma_commit(&T.ke[ks]);
           umma_commit(&T.sf[s]);
-          return true;
-        };
-        auto sums = [&](int k) {  // O += P V
+          umma_commit(&T.ke[ks]);
+        }
+      } else if (lane == 0) {
+        for (int k = 0; k < nt && ok; ++k) {  // O += P V
           const uint32_t i = n + k;
           const int s = k & 1, hb = i & 1;
-          if (!wait(&T.pf[s], (before[s] + k / 2) & 1) || !wait(&T.hf[hb], i / 2 & 1)) return false;
+          ok = wait(&T.hf[hb], i / 2 & 1) && wait(&T.pf[s], (before[s] + k / 2) & 1);
+          if (!ok) break;
           tc_fence_after();
           const uint32_t v = smem_u32(smem + kOffH) + hb * (kTok * D * 2);
 #pragma unroll
           for (int kk = 0; kk < kTok / 16; ++kk)
             umma_f16_ts(tmem + 256, tmem + 384 + 64 * s + 8 * kk,
                         sw128_mnmajor_desc(v + kk * 16 * 128, kTok * 128, 1024), idesc_f16_f32_bmn(M, D), k > 0 || kk > 0);
-          umma_commit(&T.he[hb]);
           umma_commit(&T.od[s]);
-          return true;
-        };
-        ok = wait(&T.qf, items & 1);
-        tc_fence_after();
-        if (ok) ok = scores(0) && (nt == 1 || scores(1));
-        for (int k = 0; k < nt && ok; ++k) ok = (k + 2 >= nt || scores(k + 2)) && sums(k);
-        if (ok) umma_commit(&T.of);
-        n += nt;
-        before[0] += (nt + 1) / 2;
-        before[1] += nt / 2;
+          umma_commit(&T.he[hb]);
+        }
+        if (ok) umma_commit(&T.of);  // the item's scores were all read before its last weights came
       }
+      n += nt;
+      before[0] += (nt + 1) / 2;
+      before[1] += nt / 2;
       ok = __shfl_sync(~0u, (int)ok, 0);
     }
   } else if (warp >= kWConv) {
@@ -565,16 +563,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int upto = (int)max64(min64(min64(it.hi, pos) - base + 1, kTok), 0);
         const int from = a.window > 0 ? (int)max64(min64(pos - a.window + 1 - base, kTok), 0) : 0;
         const int sinks = a.window > 0 ? (int)max64(min64(a.sinks - base, kTok), 0) : 0;
-        auto load = [&](int c, auto all, uint32_t (&x)[32]) {  // 32 scores; hidden ones -inf
-          tmem_ld32x32b_x32(sc + 32 * c, x);
+        auto load = [&](int c, auto all, uint32_t (&x)[2][32]) {  // 64 scores; hidden ones -inf
+          tmem_ld32x32b_x32(sc + 64 * c, x[0]);
+          tmem_ld32x32b_x32(sc + 64 * c + 32, x[1]);
           tmem_wait_ld();
           if (!all) {
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
-            const uint32_t there = ((present >> (2 * c) & 1) ? 0xFFFFu : 0u) | ((present >> (2 * c + 1) & 1) ? 0xFFFF0000u : 0u);
-            const uint32_t see = below(upto - 32 * c) & (~below(from - 32 * c) | below(sinks - 32 * c)) & there;
 #pragma unroll
-            for (int j = 0; j < 32; ++j)
-              if (!(see >> j & 1)) x[j] = 0xFF800000u;
+            for (int v = 0; v < 2; ++v) {
+              const int c0 = 64 * c + 32 * v;
+              const uint32_t there = ((present >> (c0 / 16) & 1) ? 0xFFFFu : 0u) | ((present >> (c0 / 16 + 1) & 1) ? 0xFFFF0000u : 0u);
+              const uint32_t see = below(upto - c0) & (~below(from - c0) | below(sinks - c0)) & there;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(see >> j & 1)) x[v][j] = 0xFF800000u;
+            }
           }
         };
         // what a block's scores are multiplied by; never 0: a hidden score, -inf, times it stays -inf
@@ -584,19 +587,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         float top = -INFINITY, topv = -INFINITY;
         auto largest = [&](auto all) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[2][32];
             load(c, all, x);
-            float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              t0 = fmaxf(t0, __uint_as_float(x[j]));
-              t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
+            for (int u = 0; u < 4; ++u) {
+              float t = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) t = fmaxf(t, __uint_as_float(x[u / 2][16 * (u % 2) + j]));
+              t *= factor(me.ks[4 * c + u]);
+              top = fmaxf(top, t);
+              topv = fmaxf(topv, t + me.ve[4 * c + u]);
             }
-            t0 *= factor(me.ks[2 * c]);
-            t1 *= factor(me.ks[2 * c + 1]);
-            top = fmaxf(top, fmaxf(t0, t1));
-            topv = fmaxf(topv, fmaxf(t0 + me.ve[2 * c], t1 + me.ve[2 * c + 1]));
           }
         };
         if (!idle) {
@@ -643,32 +645,37 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         auto weigh = [&](auto all) {
 #pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t x[32], y[16];
+          for (int c = 0; c < 2; ++c) {
+            uint32_t x[2][32];
             load(c, all, x);
-            if (c == 3) {  // S may be overwritten
+            if (c == 1) {  // S may be overwritten
               tc_fence_before();
               mbar_arrive(&T.sc[s]);
             }
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float cb = factor(me.ks[2 * c + u]), off = me.ve[2 * c + u] - mpr + kLift;
-              const uint64_t off2 = two(off, off), cb2 = two(cb, cb);
-              uint64_t sum = two(0.f, 0.f);
+            for (int v = 0; v < 2; ++v) {
+              uint32_t y[16];
 #pragma unroll
-              for (int j = 0; j < 16; j += 2) {
-                float d0, d1;
-                split(fma2(two(__uint_as_float(x[16 * u + j]), __uint_as_float(x[16 * u + j + 1])), cb2, off2), d0, d1);
-                d0 = ex2(d0);
-                d1 = ex2(d1);
-                sum = add2(sum, two(d0, d1));
-                y[8 * u + j / 2] = pack_f16(d0, d1);
+              for (int u = 0; u < 2; ++u) {
+                const int blk = 4 * c + 2 * v + u;
+                const float cb = factor(me.ks[blk]), off = me.ve[blk] - mpr + kLift;
+                const uint64_t off2 = two(off, off), cb2 = two(cb, cb);
+                uint64_t sum = two(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < 16; j += 2) {
+                  float d0, d1;
+                  split(fma2(two(__uint_as_float(x[v][16 * u + j]), __uint_as_float(x[v][16 * u + j + 1])), cb2, off2), d0, d1);
+                  d0 = ex2(d0);
+                  d1 = ex2(d1);
+                  sum = add2(sum, two(d0, d1));
+                  y[8 * u + j / 2] = pack_f16(d0, d1);
+                }
+                float s0, s1;
+                split(sum, s0, s1);
+                l = fmaf(s0 + s1, back * me.iv[blk], l);
               }
-              float s0, s1;
-              split(sum, s0, s1);
-              l = fmaf(s0 + s1, back * me.iv[2 * c + u], l);
+              tmem_st32x32b_x16(pc + 32 * c + 16 * v, y);
             }
-            tmem_st32x32b_x16(pc + 16 * c, y);
           }
         };
         if (idle) {
@@ -740,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     while (globaltimer_ns() - t0 < 200000ull) {
     }
   }
-  if (warp == kWMma) tmem_dealloc(tmem, 512);
+  if (warp == kWQk) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace
