@@ -1,8 +1,7 @@
 // kv_attention_tc.cu -- attention over the paged 8-bit cache with many query rows for a key head (a group of draft
 // tokens of many heads, a chunk of a prompt): bf16 queries, d = 128, on the tcgen05 tensor cores.
 //
-// The same sums as kv_attention.cu (two running maxima, one for the denominator and one for the numerator with the
-// values' scales), for items of 128 query rows by tiles of 128 tokens:
+// The same sums as kv_attention.cu, for items of 128 query rows by tiles of 128 tokens:
 //   S = Q K^T   kind::f8f6f4.  Keys are multiplied as they lie in the cache: TMA brings e4m3 pages into the swizzled
 //               operand layout, nothing is converted.  A bf16 query has 8 bits: two e4m3 parts of 4 bits hold it
 //               (scaled to 2^8; what lies 2^-10 below a row's largest keeps fewer), two products into one sum.
@@ -27,7 +26,7 @@ constexpr int kTileB = kTok * D;             // bytes of an e4m3 tile
 constexpr int kSoft = 256, kConv = 128;      // threads: two softmax warpgroups, one of the converters
 constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWQk = kWTma + 1, kWPv = kWQk + 1;
 constexpr int kThreads = 32 * (kWPv + 1);
-constexpr float kLift = 2.f, kSlack = 13.f;  // weights up to 2^15: the maxima may lag by 2^13 before sums are rescaled
+constexpr float kLift = 2.f;  // a weight of the row's reference is 2^2 in fp16
 
 struct Meta {  // of a tile's 8 blocks
   float ks[8], ve[8], iv[8];  // 2^ke, ve, 2^-ve
@@ -253,6 +252,13 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   return r;
 }
 
+// Values that are not to be computed with before this point.
+__device__ __forceinline__ void stay(uint32_t (&x)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 8)
+    asm volatile("" : "+r"(x[i]), "+r"(x[i + 1]), "+r"(x[i + 2]), "+r"(x[i + 3]), "+r"(x[i + 4]), "+r"(x[i + 5]), "+r"(x[i + 6]), "+r"(x[i + 7]));
+}
+
 // Whether every row of the item sees every token of a tile (where its pages are present).
 __device__ __forceinline__ bool whole_tile(const KvAttnArgs& a, const Item& it, int base) {
   return base + kTok - 1 <= min64(it.p_lo, it.hi) &&
@@ -295,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = T.tmem_slot;  // 128 columns each of S0, S1 and O, 64 each of P0, P1
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_wait(bar, parity, args.timeout_ns, &T.abort_flag)) return true;
+    if (mbar_try_wait(bar, parity) || mbar_wait_suspended(bar, parity, args.timeout_ns, &T.abort_flag)) return true;
     T.abort_flag = 1;
     atomicOr(args.line.status, DEV_ERR_TIMEOUT);
     return false;
@@ -452,25 +458,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         const uint8_t* src = smem + kOffV + vs * kTileB + t * 128;
         uint8_t* dst = smem + kOffH + hb * (kTok * D * 2) + t * 128;
-        const bool dead = base + t > w.it.hi;  // what lies behind the last token stays out of the product
         const bool look = !whole_tile(a, w.it, base);
         uint32_t odd = 0;
-#pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4 r = *reinterpret_cast<const uint4*>(src + ((c ^ (t & 7)) << 4));
-          if (dead) r = make_uint4(0, 0, 0, 0);
-          const uint32_t x[4] = {r.x, r.y, r.z, r.w};
-          uint32_t y[8];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (look) odd |= __vcmpeq4(x[j] & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
-            y[2 * j] = cvt_e4m3x2(x[j]);
-            y[2 * j + 1] = cvt_e4m3x2(x[j] >> 16);
-          }
-          uint8_t* half = dst + (c / 4) * (kTok * 128);  // dims 0-63, then 64-127
+        auto put = [&](int c, uint4 lo, uint4 hi) {  // 16 dims of fp16; dims 0-63, then 64-127
+          uint8_t* half = dst + (c / 4) * (kTok * 128);
           const int c2 = (c % 4) * 2;
-          *reinterpret_cast<uint4*>(half + ((c2 ^ (t & 7)) << 4)) = make_uint4(y[0], y[1], y[2], y[3]);
-          *reinterpret_cast<uint4*>(half + (((c2 + 1) ^ (t & 7)) << 4)) = make_uint4(y[4], y[5], y[6], y[7]);
+          *reinterpret_cast<uint4*>(half + ((c2 ^ (t & 7)) << 4)) = lo;
+          *reinterpret_cast<uint4*>(half + (((c2 + 1) ^ (t & 7)) << 4)) = hi;
+        };
+        if (base + t > w.it.hi) {  // what lies behind the last token stays out of the product
+#pragma unroll 1
+          for (int c = 0; c < 8; ++c) put(c, make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0));
+        } else {
+#pragma unroll 4
+          for (int c = 0; c < 8; ++c) {
+            const uint4 r = *reinterpret_cast<const uint4*>(src + ((c ^ (t & 7)) << 4));
+            put(c, make_uint4(cvt_e4m3x2(r.x), cvt_e4m3x2(r.x >> 16), cvt_e4m3x2(r.y), cvt_e4m3x2(r.y >> 16)),
+                make_uint4(cvt_e4m3x2(r.z), cvt_e4m3x2(r.z >> 16), cvt_e4m3x2(r.w), cvt_e4m3x2(r.w >> 16)));
+          }
+          if (look) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              const uint4 r = *reinterpret_cast<const uint4*>(src + (c << 4));
+              odd |= __vcmpeq4(r.x & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(r.y & 0x7F7F7F7Fu, 0x7F7F7F7Fu) |
+                     __vcmpeq4(r.z & 0x7F7F7F7Fu, 0x7F7F7F7Fu) | __vcmpeq4(r.w & 0x7F7F7F7Fu, 0x7F7F7F7Fu);
+            }
+          }
         }
         // A weight of zero does not hide a NaN: where some rows may not see this token, the call is computed again
         // by the kernel that goes row by row.
@@ -548,144 +561,174 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = __all_sync(~0u, ok && wait(&T.qf, items & 1));
       const float unit = T.unit[r];
       const bool idle = 32 * (warp % 4) >= it.valid;  // a warp without rows
-      float m = -INFINITY, l = 0.f;
+      // what the row sees, and what all rows do, as positions that fit 32 bits (window and first tokens: all, where
+      // there is no window)
+      auto small = [](int64_t v) { return (int)min64(max64(v, -1), 0x7FFFFFF0); };
+      const int sees_upto = small(min64(it.hi, pos)), whole_upto = small(min64(it.p_lo, it.hi));
+      const int sees_from = a.window > 0 ? max(small(pos - a.window + 1), 0) : 0;
+      const int whole_from = a.window > 0 ? max(small(it.p_hi - a.window + 1), 0) : 0;
+      const int sinks = a.window > 0 ? small(a.sinks) : 0;
+      const int tile0 = w.t0, ahead = it.ahead, gap = it.w0 - it.ahead;
+      // u: the reference of the row's weights, 2^(z + ve - u + 2) in the product, 2^(z - u + 2) in the sum l
+      float u = -INFINITY, l = 0.f;
       for (int k = s; k < nt; k += 2, ++mine) {
         const uint32_t i = n + k;
-        const int base = it.tile(w.t0 + k) * kTok;
         if (!ok) continue;
         ok = __all_sync(~0u, wait(&T.mf[i % kMeta], i / kMeta & 1) && wait(&T.sf[s], mine & 1));
         if (!ok) continue;
         tc_fence_after();
         const Meta& me = T.meta[i % kMeta];
+        const int kk = k + tile0, base = (kk < ahead ? kk : kk + gap) * kTok;
         const uint32_t present = me.present;
-        const bool whole = present == 0xFFu && whole_tile(a, it, base);
-        // which of 32 columns this row sees, where the tile is not whole
-        const int upto = (int)max64(min64(min64(it.hi, pos) - base + 1, kTok), 0);
-        const int from = a.window > 0 ? (int)max64(min64(pos - a.window + 1 - base, kTok), 0) : 0;
-        const int sinks = a.window > 0 ? (int)max64(min64(a.sinks - base, kTok), 0) : 0;
-        auto load = [&](int c, auto all, uint32_t (&x)[2][32]) {  // 64 scores; hidden ones -inf
-          tmem_ld32x32b_x32(sc + 64 * c, x[0]);
-          tmem_ld32x32b_x32(sc + 64 * c + 32, x[1]);
+        const bool whole = present == 0xFFu && base + kTok - 1 <= whole_upto && (base >= whole_from || base + kTok <= sinks);
+        auto load = [&](int c, auto all, uint32_t (&x)[32]) {  // 32 scores; hidden ones -inf
+          tmem_ld32x32b_x32(sc + 32 * c, x);
           tmem_wait_ld();
           if (!all) {
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
+            const int c0 = base + 32 * c;
+            const uint32_t there = ((present >> (2 * c) & 1) ? 0xFFFFu : 0u) | ((present >> (2 * c + 1) & 1) ? 0xFFFF0000u : 0u);
+            const uint32_t see = below(sees_upto - c0 + 1) & (~below(sees_from - c0) | below(sinks - c0)) & there;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              const int c0 = 64 * c + 32 * v;
-              const uint32_t there = ((present >> (c0 / 16) & 1) ? 0xFFFFu : 0u) | ((present >> (c0 / 16 + 1) & 1) ? 0xFFFF0000u : 0u);
-              const uint32_t see = below(upto - c0) & (~below(from - c0) | below(sinks - c0)) & there;
-#pragma unroll
-              for (int j = 0; j < 32; ++j)
-                if (!(see >> j & 1)) x[v][j] = 0xFF800000u;
-            }
+            for (int j = 0; j < 32; ++j)
+              if (!(see >> j & 1)) x[j] = 0xFF800000u;
           }
         };
         // what a block's scores are multiplied by; never 0: a hidden score, -inf, times it stays -inf
         auto factor = [&](float ks) { return fmaxf(unit * ks, 1e-37f); };
-        // The loops are not unrolled, and masked tiles have code of their own: the code then stays in the instruction
-        // cache (unrolled it ran at half the speed; in one copy the compiler masks every tile).
-        float top = -INFINITY, topv = -INFINITY;
-        auto largest = [&](auto all) {
-#pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[2][32];
-            load(c, all, x);
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              float t = -INFINITY;
-#pragma unroll
-              for (int j = 0; j < 16; ++j) t = fmaxf(t, __uint_as_float(x[u / 2][16 * (u % 2) + j]));
-              t *= factor(me.ks[4 * c + u]);
-              top = fmaxf(top, t);
-              topv = fmaxf(topv, t + me.ve[4 * c + u]);
-            }
+        // One pass: weights relative to the reference u that is known when the tile begins.  It may lag behind the
+        // largest score as long as fp16 holds the weights (32 of them sum to 2^15 at most); a row for which it does not,
+        // or that has none yet, takes a new one from the scores in hand, and what it weighed before is scaled down.
+        // After an item's first tiles that is rare.  (The loops are not unrolled, and masked tiles have code of their
+        // own: the code then stays in the instruction cache.  Unrolled it ran at half the speed, and in one copy the
+        // compiler masks every tile.)
+        if (k >= 2) {
+          const float known = T.ref[r];  // of the tile before, or still of the one before that: settled at the end
+          if (known > u) {
+            l *= ex2(u - known);
+            u = known;
           }
-        };
-        if (!idle) {
-          if (whole) largest(std::true_type{});
-          else largest(std::false_type{});
         }
-        // The weights' reference m' (and m, the sum's) may lag behind the largest score by 2^13; where it would by
-        // more, the output sums so far are scaled down, after the tile before has gone into them.  After the first
-        // tiles of an item that is rare.
-        if (k > 0) {
-          ok = __all_sync(~0u, wait(&T.rf[s ^ 1], (theirs + (k - 1) / 2) & 1));
-          if (!ok) continue;
-        }
-        float mp = k > 0 ? T.ref[r] : -INFINITY;
-        const bool up = topv > mp + kSlack;
-        const float f = up && mp != -INFINITY ? ex2(mp - topv) : 1.f;
-        if (up) mp = topv;
-        T.ref[r] = mp;
-        mbar_arrive(&T.rf[s]);
-        if (__any_sync(~0u, f != 1.f)) {
-          ok = __all_sync(~0u, wait(&T.od[s ^ 1], (theirs + (k - 1) / 2) & 1));
-          if (!ok) continue;
-          tc_fence_after();
+        auto scale_weights = [&](int columns, float f) {  // this tile's first ones
+          const __half2 fh = __float2half2_rn(f);
+          tmem_wait_st();
 #pragma unroll 1
-          for (int q = 0; q < D / 16; ++q) {
+          for (int q = 0; q < columns; q += 16) {
             uint32_t y[16];
-            tmem_ld32x32b_x16(oc + 16 * q, y);
+            tmem_ld32x32b_x16(pc + q, y);
             tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * f);
-            tmem_st32x32b_x16(oc + 16 * q, y);
+            for (int j = 0; j < 16; ++j) {
+              const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[j]), fh);
+              y[j] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            tmem_st32x32b_x16(pc + q, y);
           }
-        }
-        if (top > m + kSlack) {
-          l *= m == -INFINITY ? 1.f : ex2(m - top);
-          m = top;
-        }
-        const float mpr = mp == -INFINITY ? 0.f : mp;
-        const float back = ex2(mpr - kLift - (m == -INFINITY ? 0.f : m));  // product's weights to the sum's, but for 2^-ve
-        if (k >= 2) {  // this half's weights of two tiles ago have been multiplied
-          ok = __all_sync(~0u, wait(&T.od[s], (mine - 1) & 1));
-          if (!ok) continue;
-          tc_fence_after();
-        }
+        };
         auto weigh = [&](auto all) {
 #pragma unroll 1
-          for (int c = 0; c < 2; ++c) {
-            uint32_t x[2][32];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t x[32], y[16];
             load(c, all, x);
-            if (c == 1) {  // S may be overwritten
+            if (c == 3) {  // S may be overwritten
               tc_fence_before();
               mbar_arrive(&T.sc[s]);
             }
+            const float2 ks = *reinterpret_cast<const float2*>(&me.ks[2 * c]), ve = *reinterpret_cast<const float2*>(&me.ve[2 * c]),
+                         iv = *reinterpret_cast<const float2*>(&me.iv[2 * c]);
+            const float cb[2] = {factor(ks.x), factor(ks.y)};
+            float part = 0.f;
+#pragma unroll 1
+            for (bool first = true;; first = false) {
+              const float ref = u == -INFINITY ? 0.f : u;
+              float total = 0.f;
+              part = 0.f;
 #pragma unroll
-            for (int v = 0; v < 2; ++v) {
-              uint32_t y[16];
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const int blk = 4 * c + 2 * v + u;
-                const float cb = factor(me.ks[blk]), off = me.ve[blk] - mpr + kLift;
-                const uint64_t off2 = two(off, off), cb2 = two(cb, cb);
+              for (int h = 0; h < 2; ++h) {
+                const float off = (h ? ve.y : ve.x) - ref + kLift;
+                const uint64_t off2 = two(off, off), cb2 = two(cb[h], cb[h]);
                 uint64_t sum = two(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < 16; j += 2) {
                   float d0, d1;
-                  split(fma2(two(__uint_as_float(x[v][16 * u + j]), __uint_as_float(x[v][16 * u + j + 1])), cb2, off2), d0, d1);
+                  split(fma2(two(__uint_as_float(x[16 * h + j]), __uint_as_float(x[16 * h + j + 1])), cb2, off2), d0, d1);
                   d0 = ex2(d0);
                   d1 = ex2(d1);
                   sum = add2(sum, two(d0, d1));
-                  y[8 * u + j / 2] = pack_f16(d0, d1);
+                  y[8 * h + j / 2] = pack_f16(d0, d1);
                 }
                 float s0, s1;
                 split(sum, s0, s1);
-                l = fmaf(s0 + s1, back * me.iv[blk], l);
+                total += s0 + s1;
+                part = fmaf(s0 + s1, h ? iv.y : iv.x, part);
               }
-              tmem_st32x32b_x16(pc + 32 * c + 16 * v, y);
+              const bool over = total > 32768.f || (first && u == -INFINITY);
+              if (!__any_sync(~0u, over)) break;
+              stay(x);  // or the compiler takes the maxima of every tile
+              float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+              for (int j = 0; j < 16; ++j) {
+                t0 = fmaxf(t0, __uint_as_float(x[j]));
+                t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
+              }
+              const float t = fmaxf(t0 * cb[0] + ve.x, t1 * cb[1] + ve.y);
+              const bool raise = over && t > u;
+              if (!__any_sync(~0u, raise)) break;
+              const float f = raise && u != -INFINITY ? ex2(u - t) : 1.f;
+              if (raise) u = t;
+              l *= f;
+              if (c > 0) scale_weights(16 * c, f);
             }
+            l += part;
+            if (c == 0 && k >= 2) {  // this half's weights of two tiles ago are used up
+              ok = wait(&T.od[s], (mine - 1) & 1);
+              tc_fence_after();
+            }
+            tmem_st32x32b_x16(pc + 16 * c, y);
           }
         };
         if (idle) {
           tc_fence_before();
           mbar_arrive(&T.sc[s]);
+        } else if (whole) {
+          weigh(std::true_type{});
         } else {
-          if (whole) weigh(std::true_type{});
-          else weigh(std::false_type{});
-          tmem_wait_st();
+          weigh(std::false_type{});
         }
+        ok = __all_sync(~0u, ok);
+        if (!ok) continue;
+        // The rows' reference, settled tile after tile: the larger of the tile before's and this one's.
+        float before = -INFINITY;
+        if (k > 0) {
+          ok = __all_sync(~0u, wait(&T.rf[s ^ 1], (theirs + (k - 1) / 2) & 1));
+          if (!ok) continue;
+          before = T.ref[r];
+        }
+        const float settled = fmaxf(u, before);
+        const float fw = settled > u && u != -INFINITY ? ex2(u - settled) : 1.f;
+        const float fo = settled > before && before != -INFINITY ? ex2(before - settled) : 1.f;
+        T.ref[r] = settled;
+        mbar_arrive(&T.rf[s]);
+        if (__any_sync(~0u, fw != 1.f)) {
+          l *= fw;
+          scale_weights(64, fw);
+        }
+        u = settled;
+        if (__any_sync(~0u, fo != 1.f)) {  // the sums so far, once the tile before has gone into them
+          ok = __all_sync(~0u, wait(&T.od[s ^ 1], (theirs + (k - 1) / 2) & 1));
+          if (!ok) continue;
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D; q += 16) {
+            uint32_t y[16];
+            tmem_ld32x32b_x16(oc + q, y);
+            tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * fo);
+            tmem_st32x32b_x16(oc + q, y);
+          }
+        }
+        tmem_wait_st();
         tc_fence_before();
         mbar_arrive(&T.pf[s]);
       }
@@ -693,17 +736,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       // the item's sums: each warpgroup takes half of the dims
       ok = __all_sync(~0u, ok && wait(&T.of, items & 1));
       tc_fence_after();
-      T.stats[s][r][0] = m;
+      T.stats[s][r][0] = u;
       T.stats[s][r][1] = l;
       mbar_arrive(&T.xf);
       ok = __all_sync(~0u, ok && wait(&T.xf, items & 1));
       if (ok && !idle) {
-        const float mpt = T.ref[r], m0 = T.stats[0][r][0], m1 = T.stats[1][r][0], l0 = T.stats[0][r][1], l1 = T.stats[1][r][1];
-        const float mt = fmaxf(m0, m1);
-        const float lt = (m0 == -INFINITY ? l0 : l0 * ex2(m0 - mt)) + (m1 == -INFINITY ? l1 : l1 * ex2(m1 - mt));
-        const bool none = mpt == -INFINITY && lt == 0.f;  // the row saw nothing
+        const float ref = T.ref[r], u0 = T.stats[0][r][0], u1 = T.stats[1][r][0], l0 = T.stats[0][r][1], l1 = T.stats[1][r][1];
+        // a half that saw nothing has l = 0, or NaN of a score
+        const float lt = (u0 == -INFINITY ? l0 : l0 * ex2(u0 - ref)) + (u1 == -INFINITY ? l1 : l1 * ex2(u1 - ref));
+        const bool none = ref == -INFINITY && lt == 0.f;  // the row saw nothing
         const bool all = w.t0 == 0 && w.t1 == it.tiles;
-        const float g = all && !none ? ex2(mpt - mt - kLift) / lt : 1.f;
+        const float g = all && !none ? 1.f / lt : 1.f;
         const int rr = it.rr0 + r;
         const int64_t row = it.row0 + rr / a.group;
         const int j = it.h * a.group + rr % a.group;
@@ -728,9 +771,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (put && s == 0) {
           if (all) {
-            if (a.lse) a.lse[row * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (mt + log2f(lt));
+            if (a.lse) a.lse[row * a.hq + j] = none ? -INFINITY : 0.6931471805599453f * (ref - kLift + log2f(lt));
           } else {
-            *reinterpret_cast<float4*>(part + M * D + r * 4) = make_float4(mpt, mt, lt, 0.f);
+            *reinterpret_cast<float4*>(part + M * D + r * 4) = make_float4(ref, ref, lt * ex2(-kLift), 0.f);
           }
         }
         if (tid == 0 && !all && w.t0 == 0)
