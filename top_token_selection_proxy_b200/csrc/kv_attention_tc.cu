@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = T.tmem_slot;  // 128 columns each of S0, S1 and O, 64 each of P0, P1
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    if (mbar_try_wait(bar, parity) || mbar_wait_suspended(bar, parity, args.timeout_ns, &T.abort_flag)) return true;
+    if (mbar_wait(bar, parity, args.timeout_ns, &T.abort_flag)) return true;
     T.abort_flag = 1;
     atomicOr(args.line.status, DEV_ERR_TIMEOUT);
     return false;
