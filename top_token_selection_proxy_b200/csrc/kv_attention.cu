@@ -3,8 +3,9 @@
 //
 // o = sum_s p_s v_s / sum_s p_s, p_s = 2^(z_s - m), z = scale2 * q . k (units of log 2), one pass over the keys.
 // A key is payload * 2^e with one e for 16 tokens and head, so z = (q . payload) * 2^e scale2, and the output sum
-// takes weights p * 2^e.  Two running maxima keep both sums in range whatever the scales are: m of z for the
-// denominator, m' of z + e for the numerator.  Weights enter the product as fp16 values of 2^14 2^(z + e - m').
+// takes weights p * 2^e.  Both sums are kept relative to a reference u of each row, a value of z + e that may lag
+// behind the largest by as much as fp16 holds: weights enter the product as fp16 values of 2^(z + e - u + 2), the
+// denominator adds 2^(z - u) in fp32, which holds it for all scales there are (|e| <= 60).
 //
 // What bounds it: the cache's bytes (2 d and a little for each token and key head, read once for up to 16 query
 // rows).  So the payload goes to registers in the order in which the matrix instruction wants it, without a
@@ -27,13 +28,19 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRowsT = 16;              // query rows of an item
 constexpr int kWTok = 32;               // tokens a warp takes at a time (two blocks)
 constexpr int kTile = kWTok * kWarps;   // tokens of a tile
-constexpr float kLift = 2.f, kSlack = 13.f;  // weights up to 2^15: the maxima may lag by 2^13 before sums are rescaled
+constexpr float kLift = 2.f;            // a weight of the row's reference is 2^2 in fp16
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Values that are not to be computed with before this point.
+__device__ __forceinline__ void stay(float (&z)[4][4]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) asm volatile("" : "+f"(z[j][0]), "+f"(z[j][1]), "+f"(z[j][2]), "+f"(z[j][3]));
 }
 
 __device__ __forceinline__ float quad_max(float x) {
@@ -91,7 +98,7 @@ struct Shape {
   static constexpr int kStageBytes = 32 * (kKPieces * 16 + 8 * kVBytes + 4);  // a warp's; 4: the tokens' scales
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kQParts = BF16 ? 1 : 3;
-  static constexpr int kQBytes = BF16 ? 0 : kQParts * (D / 16) * 32 * 16;
+  static constexpr int kQBytes = kQParts * (D / 16) * 32 * 16;  // the query rows' operands, the same for all warps
   static constexpr size_t kBytes = kRing + kQBytes + 64 * sizeof(float) * kWarps;
 };
 
@@ -194,8 +201,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 
     // q: this lane's operands, scaled by a power of two so that the row's largest lies in [2^14, 2^15): one fp16 holds
     // a bf16's 8 bits (down to 2^-31 of the largest), three hold an fp32's 24.
-    uint32_t qa[BF16 ? NK : 1][4];
-    float unit[2];  // scale2 / that power
+    float unit[2];  // |scale2| / that power
     {
       float v[2][2 * NK * 2];
       uint4* const qs = reinterpret_cast<uint4*>(smem + S::kRing);
@@ -230,25 +236,19 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
         top = quad_max(top);
         const bool finite = top <= 3.402823466e38f;
         const int ex = top > 0.f && finite ? max((int)(__float_as_uint(top) >> 23) - 127 - 14, -100) : 0;
-        unit[i] = a.scale2 * kv_exp2i(ex);
-        const float down = kv_exp2i(-ex);
+        unit[i] = fabsf(a.scale2) * kv_exp2i(ex);
+        const float down = a.scale2 < 0.f ? -kv_exp2i(-ex) : kv_exp2i(-ex);
 #pragma unroll
         for (int k = 0; k < D / 4; ++k) v[i][k] *= down;
       }
-      if (BF16) {
-#pragma unroll
-        for (int ks = 0; ks < NK; ++ks)
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // a0: row g, a1: row g + 8, a2, a3: the same rows' next two dims
-            qa[BF16 ? ks : 0][k] = pack_f16(v[k & 1][4 * ks + (k & 2)], v[k & 1][4 * ks + (k & 2) + 1]);
-      } else if (warp == 0) {  // kept in shared memory
+      if (warp == 0) {
 #pragma unroll
         for (int ks = 0; ks < NK; ++ks)
 #pragma unroll
           for (int part = 0; part < S::kQParts; ++part) {
             uint32_t w[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
+            for (int k = 0; k < 4; ++k) {  // a0: row g, a1: row g + 8, a2, a3: the same rows' next two dims
               float* f = &v[k & 1][4 * ks + (k & 2)];
               w[k] = pack_f16(f[0], f[1]);
               const __half2 hh = *reinterpret_cast<const __half2*>(&w[k]);
@@ -258,10 +258,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
             qs[(part * NK + ks) * 32 + lane] = make_uint4(w[0], w[1], w[2], w[3]);
           }
       }
-      if (!BF16) __syncthreads();
+      __syncthreads();
     }
 
-    float o[NT][4], m[2] = {-INFINITY, -INFINITY}, mp[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f}, back[2] = {1.f, 1.f};
+    float o[NT][4], ref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < NT; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
 
@@ -287,22 +287,30 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       return tile * kTile + warp * kWTok;
     };
 
-    // Look-ups run ahead of the copies: list entries (selected), then pages, then the copies and the exponents.
+    // Look-ups run ahead of the copies, a step between each and the next: list entries (selected), then pages, then the
+    // copies and the scales.  What a load brings is not looked at before the step after.
     const int32_t* const list = SEL ? a.indices + row0 * a.idx_stride : nullptr;
-    auto load_entry = [&](int step) -> int {  // a lane's position of a step; -1: none
-      if (step >= steps) return -1;
-      const int i = base_of(step) + lane;
-      if (!SEL) return i;
-      const int s = i < a.topk ? __ldg(list + i) : -1;
-      return s <= hi ? s : -1;
+    auto load_entry = [&](int step) -> int {  // a lane's position of a step, as the list has it
+      int i = -1;
+      if (step < steps) i = base_of(step) + lane;
+      if (SEL) {
+        int s = -1;
+        if (i >= 0 && i < a.topk) s = __ldg(list + i);
+        return s;
+      }
+      return i;
     };
-    auto load_page = [&](int s) -> int {  // page of a lane's position; -1: absent
-      if (s < 0 || s > hi) return -1;
-      return kv_page(a.st, a.c, b, (uint32_t)s);
+    const int32_t* const table = a.st.table + (int64_t)max(b, 0) * a.st.stride;
+    auto load_page = [&](int s) -> int {  // page of a lane's position, as the table has it; -1: there is none
+      int page = -1;
+      const uint32_t i = (uint32_t)max(s, 0) / (uint32_t)a.c.ps;
+      if (s >= 0 && s <= hi && i < (uint32_t)a.st.width) page = __ldg(table + i);
+      return page;
     };
     // The copies of one step, and the loads of the lane's token's scales.  They are kept beside the copies: ke + 127 in
     // the low byte, ve as bf16 in the upper half; 0 where the token is absent.
     int pend_ke = 0, pend_ve = 0;
+    bool pend_there = false;
     uint32_t pend_at = 0;
     auto issue = [&](int step, int s, int page) {
       const uint32_t at_stage = (step % kStages) * S::kStageBytes;
@@ -310,33 +318,40 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       uint32_t in = 0;
       int slot = -1;  // row of the cache
       pend_at = at_stage;
-      pend_ke = pend_ve = 0;
-      if (page >= 0) {
+      pend_there = page >= 0 && page < a.c.pages;
+      if (pend_there) {
         in = (uint32_t)s % (uint32_t)a.c.ps;
         const int ph = page * a.c.hk + h;
         slot = ph * a.c.ps + (int)in;
         const int64_t be = (int64_t)ph * (a.c.ps / kKvBlock) + in / kKvBlock;
-        pend_ke = 0x100 | (uint8_t)__ldg(a.c.ke + be);  // not waited for here
+        pend_ke = __ldg(a.c.ke + be);
         pend_ve = __ldg(a.c.ve + be);
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int sl = __shfl_sync(~0u, slot, 8 * j + g);
-        const uint8_t* src = a.c.k + ((int64_t)max(sl, 0) * D + 16 * tig);
-#pragma unroll
-        for (int c = 0; c < D / 64; ++c)
-          cp_async_or_zero<16>(dst + (j * (D / 64) + c) * 512, src + 64 * c, sl >= 0);
-      }
       const uint32_t vdst = ring + at_stage + S::kKPieces * 512 + lane * S::kVBytes;
+      const uint8_t* const ksrc = a.c.k + 16 * tig;
+      const uint8_t* const vsrc = a.c.v + S::kVBytes * g;
+      auto copies = [&](auto every) {  // every token is there
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const int sl = __shfl_sync(~0u, slot, 16 * (j / 4) + 8 * (j / 2 % 2) + 2 * tig + j % 2);
-        cp_async_or_zero<S::kVBytes>(vdst + j * 32 * S::kVBytes, a.c.v + ((int64_t)max(sl, 0) * D + S::kVBytes * g), sl >= 0);
-      }
+        for (int j = 0; j < 4; ++j) {
+          const int sl = __shfl_sync(~0u, slot, 8 * j + g);
+          const uint8_t* src = ksrc + (int64_t)(uint32_t)(every ? sl : max(sl, 0)) * D;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+            cp_async_or_zero<16>(dst + (j * (D / 64) + c) * 512, src + 64 * c, every || sl >= 0);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int sl = __shfl_sync(~0u, slot, 16 * (j / 4) + 8 * (j / 2 % 2) + 2 * tig + j % 2);
+          cp_async_or_zero<S::kVBytes>(vdst + j * 32 * S::kVBytes, vsrc + (int64_t)(uint32_t)(every ? sl : max(sl, 0)) * D,
+                                       every || sl >= 0);
+        }
+      };
+      if (__all_sync(~0u, slot >= 0)) copies(std::true_type{});
+      else copies(std::false_type{});
     };
     // The scales of the copies issued last, one step later.
     auto settle = [&]() {
-      const uint32_t ex = pend_ke ? (uint32_t)(max((int)(int8_t)pend_ke, -126) + 127) | __float_as_uint((float)pend_ve) : 0u;
+      const uint32_t ex = pend_there ? (uint32_t)(max(pend_ke, -126) + 127) | __float_as_uint((float)pend_ve) : 0u;
       *reinterpret_cast<uint32_t*>(smem + (ring - smem_u32(smem)) + pend_at + S::kKPieces * 512 + 256 * S::kVBytes + lane * 4) = ex;
     };
 
@@ -373,27 +388,21 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
             b0[j] = cvt_e4m3x2(w);
             b1[j] = cvt_e4m3x2(w >> 16);
           }
-          if (BF16) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mma16816(z[j], qa[BF16 ? 4 * c + k : 0], b0[j], b1[j]);
-          } else {
+          for (int part = S::kQParts - 1; part >= 0; --part) {
+            const uint4 w = reinterpret_cast<const uint4*>(smem + S::kRing)[(part * NK + 4 * c + k) * 32 + lane];
+            const uint32_t aq[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int part = S::kQParts - 1; part >= 0; --part) {
-              const uint4 w = reinterpret_cast<const uint4*>(smem + S::kRing)[(part * NK + 4 * c + k) * 32 + lane];
-              const uint32_t aq[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-              for (int j = 0; j < 4; ++j) mma16816(z[j], aq, b0[j], b1[j]);
-            }
+            for (int j = 0; j < 4; ++j) mma16816(z[j], aq, b0[j], b1[j]);
           }
         }
       }
 
-      // scale, mask
-      float top[2] = {-INFINITY, -INFINITY}, topv[2] = {-INFINITY, -INFINITY};
-      uint32_t te[4][2];  // scales of the two tokens that this lane holds in each tile
+      // mask
       const bool whole = __all_sync(~0u, scales[lane] != 0) &&
                          (SEL || (base + kWTok - 1 <= min64(p_lo, hi) &&
                                   (a.window <= 0 || base > p_hi - a.window || base + kWTok <= a.sinks)));
+      uint32_t te[4][2];  // scales of the two tokens that this lane holds in each tile
       if (SEL) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -405,15 +414,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
         for (int j = 0; j < 4; j += 2)  // a block's tokens share one
           te[j][0] = te[j][1] = te[j + 1][0] = te[j + 1][1] = scales[8 * j];
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float ks = __uint_as_float(te[j][k] << 23);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) z[j][2 * i + k] *= unit[i] * ks;
-        }
       if (!whole) {
+        stay(z);  // or the compiler masks every step
 #pragma unroll
         for (int j = 0; j < 4; ++j)
 #pragma unroll
@@ -427,73 +429,74 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
             }
           }
       }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float ve = __uint_as_float(te[j][k] & 0xFFFF0000u);
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            top[i] = fmaxf(top[i], z[j][2 * i + k]);
-            topv[i] = fmaxf(topv[i], z[j][2 * i + k] + ve);
-          }
-        }
       // some row sees a token of this step that another does not
       const bool part_seen = !SEL && !whole;
 
-      // the running maxima, which may lag; the four lanes of a row hold the same
-      bool up = false;
+      // weights: p for the sum, p * 2^(ve + 2) for the product.  Where a row's do not fit fp16, or it has no reference
+      // yet, it takes a new one from the scores in hand, and its sums so far are scaled down.
+      uint32_t pa[2][4], pb[2][4];  // operands of the two blocks; the rest of them (fp32)
+      float psum[2];
+#pragma unroll 1
+      for (bool fresh = true;; fresh = false) {
+        const float r0 = ref[0] == -INFINITY ? 0.f : ref[0], r1 = ref[1] == -INFINITY ? 0.f : ref[1];
+        float wsum[2] = {0.f, 0.f};
+        psum[0] = psum[1] = 0.f;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) up |= top[i] > m[i] + kSlack || topv[i] > mp[i] + kSlack;
-      if (__any_sync(~0u, up)) {
-        bool scaled = false;
+        for (int j = 0; j < 4; ++j) {
+          float w[2][2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float ks = __uint_as_float(te[j][k] << 23), vs = ex2(__uint_as_float(te[j][k] & 0xFFFF0000u) + kLift);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              // a factor of 0 would make a hidden score, -inf, NaN
+              const float p = ex2(fmaf(z[j][2 * i + k], fmaxf(unit[i] * ks, 1e-37f), i ? -r1 : -r0));
+              psum[i] += p;
+              w[i][k] = p * vs;
+              wsum[i] += w[i][k];
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t hw = pack_f16(w[i][0], w[i][1]);
+            pa[j / 2][2 * (j % 2) + i] = hw;
+            if (!BF16) {
+              const __half2 hh = *reinterpret_cast<const __half2*>(&hw);
+              pb[j / 2][2 * (j % 2) + i] = pack_f16(w[i][0] - __low2float(hh), w[i][1] - __high2float(hh));
+            }
+          }
+        }
+        bool over[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) over[i] = wsum[i] > 32768.f || (fresh && ref[i] == -INFINITY);
+        if (!__any_sync(~0u, over[0] || over[1])) break;
+        stay(z);
+        bool raised = false;
         float f[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const float mn = quad_max(top[i]), mpn = quad_max(topv[i]);
-          if (mn > m[i] + kSlack) {
-            if (m[i] != -INFINITY) l[i] *= ex2(m[i] - mn);
-            m[i] = mn;
-          }
-          f[i] = 1.f;
-          if (mpn > mp[i] + kSlack) {
-            if (mp[i] != -INFINITY) f[i] = ex2(mp[i] - mpn);
-            mp[i] = mpn;
-          }
-          scaled |= f[i] != 1.f;
-          back[i] = ex2((m[i] == -INFINITY ? 0.f : m[i]) - (mp[i] == -INFINITY ? 0.f : mp[i]) + kLift);
+          float t = -INFINITY;
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+              t = fmaxf(t, fmaf(z[j][2 * i + k], fmaxf(unit[i] * __uint_as_float(te[j][k] << 23), 1e-37f),
+                                __uint_as_float(te[j][k] & 0xFFFF0000u)));
+          t = quad_max(t);  // the four lanes of a row decide together
+          const bool raise = quad_max(over[i] ? 1.f : 0.f) > 0.f && t > ref[i];
+          f[i] = raise && ref[i] != -INFINITY ? ex2(ref[i] - t) : 1.f;
+          if (raise) ref[i] = t;
+          l[i] *= f[i];
+          raised |= raise;
         }
-        if (__any_sync(~0u, scaled)) {
+        if (!__any_sync(~0u, raised)) break;
+        if (__any_sync(~0u, f[0] != 1.f || f[1] != 1.f)) {
 #pragma unroll
           for (int n8 = 0; n8 < NT; ++n8) o[n8][0] *= f[0], o[n8][1] *= f[0], o[n8][2] *= f[1], o[n8][3] *= f[1];
         }
       }
-      // weights: p for the sum, p * 2^(m - m' + 2) * 2^ve for the product
-      uint32_t pa[2][4], pb[2][4];  // operands of the two blocks; the rest of them (fp32)
-      const float lift[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        float w[2][2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float vs = ex2(__uint_as_float(te[j][k] & 0xFFFF0000u));
-#pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            const float p = ex2(z[j][2 * i + k] - lift[i]);
-            l[i] += p;
-            w[i][k] = p * back[i] * vs;
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const uint32_t hw = pack_f16(w[i][0], w[i][1]);
-          pa[j / 2][2 * (j % 2) + i] = hw;
-          if (!BF16) {
-            const __half2 hh = *reinterpret_cast<const __half2*>(&hw);
-            pb[j / 2][2 * (j % 2) + i] = pack_f16(w[i][0] - __low2float(hh), w[i][1] - __high2float(hh));
-          }
-        }
-      }
+      l[0] += psum[0];
+      l[1] += psum[1];
 
       // output sums: 16 tokens a block, NT tiles of 8 dims
       constexpr int VW = S::kVBytes / 4;  // words a lane holds of a value
@@ -589,7 +592,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float* st = stats + warp * 64 + (g + 8 * i) * 4;
-        st[0] = mp[i], st[1] = m[i], st[2] = l[i];
+        st[0] = ref[i], st[1] = l[i];
       }
     }
     __syncthreads();  // also: every warp is done with its ring
@@ -600,18 +603,17 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       float top = -INFINITY;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, stats[w * 64 + r * 4]);
-      const float f = mp[i] == -INFINITY ? 0.f : ex2(mp[i] - top);
       // a row that saw nothing here has sums of zero, whatever its queries are
+      const bool none = ref[i] == -INFINITY && l[i] == 0.f;
+      const float f = ref[i] == -INFINITY ? 1.f : ex2(ref[i] - top);
       float* to = sums + (warp * kRowsT + r) * D + 2 * NT * tig;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int n8 = 0; n8 < NT; n8 += 4)
           *reinterpret_cast<float4*>(to + k * NT + n8) =
-              make_float4(mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8][2 * i + k] * f,
-                          mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8 + 1][2 * i + k] * f,
-                          mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8 + 2][2 * i + k] * f,
-                          mp[i] == -INFINITY && l[i] == 0.f ? 0.f : o[n8 + 3][2 * i + k] * f);
+              make_float4(none ? 0.f : o[n8][2 * i + k] * f, none ? 0.f : o[n8 + 1][2 * i + k] * f,
+                          none ? 0.f : o[n8 + 2][2 * i + k] * f, none ? 0.f : o[n8 + 3][2 * i + k] * f);
     }
     __syncthreads();
     const bool all = t0 == 0 && t1 == e.tiles;
@@ -619,31 +621,30 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
     constexpr int kLanes = D / 4;  // threads of a row
     for (int r = tid / kLanes; r < valid; r += kThreads / kLanes) {
       const int c = tid % kLanes * 4;
-      float mt = -INFINITY, mpt = -INFINITY, lt = 0.f;
+      float top = -INFINITY, lt = 0.f;
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        mpt = fmaxf(mpt, stats[w * 64 + r * 4]);
-        mt = fmaxf(mt, stats[w * 64 + r * 4 + 1]);
+        top = fmaxf(top, stats[w * 64 + r * 4]);
         const float4 v = *reinterpret_cast<const float4*>(sums + (w * kRowsT + r) * D + c);
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
       }
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float ml = stats[w * 64 + r * 4 + 1], lw = stats[w * 64 + r * 4 + 2];
-        lt += ml == -INFINITY ? lw : lw * ex2(ml - mt);  // -inf: zero, or NaN of a score
+        const float rw = stats[w * 64 + r * 4], lw = stats[w * 64 + r * 4 + 1];
+        lt += rw == -INFINITY ? lw : lw * ex2(rw - top);  // -inf: zero, or NaN of a score
       }
       if (all) {
         const int64_t rr = row0 + (rr0 + r) / a.group;
         if (rr < a.st.rows) {
           const int j = h * a.group + (rr0 + r) % a.group;
-          const float f = lt == 0.f ? 0.f : ex2(mpt - mt - kLift) / lt;
+          const float f = lt == 0.f ? 0.f : ex2(-kLift) / lt;
           kv_store4(a, (rr * a.hq + j) * (int64_t)D + c, s.x * f, s.y * f, s.z * f, s.w * f, BF16);
-          if (a.lse && c == 0) a.lse[rr * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (mt + log2f(lt));
+          if (a.lse && c == 0) a.lse[rr * a.hq + j] = lt == 0.f ? -INFINITY : 0.6931471805599453f * (top + log2f(lt));
         }
       } else {
         *reinterpret_cast<float4*>(part + r * D + c) = s;
-        if (c == 0) *reinterpret_cast<float4*>(part + kRowsT * D + r * 4) = make_float4(mpt, mt, lt, 0.f);
+        if (c == 0) *reinterpret_cast<float4*>(part + kRowsT * D + r * 4) = make_float4(top, top, lt, 0.f);
       }
     }
     if (!all && t0 == 0 && tid == 0)
