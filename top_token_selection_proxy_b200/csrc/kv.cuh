@@ -65,8 +65,8 @@ struct alignas(16) KvOpen {
   int32_t stretch, head0, rr0, valid, open;  // open: how many CTAs' results make the item (0: none was begun)
 };
 
-// The CTA after the last one whose stretch reaches into an item that ends at `item_end`: stretch j begins at
-// total * j / ctas.
+// The CTA after the last one whose stretch reaches into an item that ends at place `item_end` of the line: stretch j
+// begins at total * j / ctas.
 __device__ __forceinline__ int kv_parts(int64_t item_end, int64_t total, int64_t ctas) {
   return (int)((item_end * ctas + total - 1) / total);
 }

@@ -15,7 +15,8 @@
 // memory (cp.async), so the ring needs no barrier: every warp runs through its own tokens alone.
 //
 // Work is cut evenly whatever the lengths are: all tiles of 128 tokens of all (sequence, key head, 16 query rows)
-// stand in one line, and every CTA takes an equal stretch of it.  A stretch that begins or ends inside an item
+// stand in one line, each item behind a few places for what it costs beside its tiles, and every CTA takes an equal
+// stretch of it.  A stretch that begins or ends inside an item
 // leaves a partial result, which kv_merge_kernel joins in a fixed order.
 #include <type_traits>
 
@@ -28,6 +29,7 @@ constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kRowsT = 16;              // query rows of an item
 constexpr int kWTok = 32;               // tokens a warp takes at a time (two blocks)
 constexpr int kTile = kWTok * kWarps;   // tokens of a tile
+constexpr int kItemCost = 4;            // what an item costs beside its tiles, in tiles
 constexpr float kLift = 2.f;            // a weight of the row's reference is 2^2 in fp16
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -86,7 +88,7 @@ __device__ __forceinline__ Extent extent_of(const KvAttnArgs& a, int b) {
 __device__ __forceinline__ int64_t weight_of(const KvAttnArgs& a, int b) {
   if (b >= a.st.B) return 0;
   const Extent e = extent_of(a, b);
-  return (int64_t)a.c.hk * e.row_tiles * e.tiles;
+  return (int64_t)a.c.hk * e.row_tiles * (e.tiles + kItemCost);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -100,6 +102,8 @@ struct Shape {
   static constexpr int kQParts = BF16 ? 1 : 3;
   static constexpr int kQBytes = kQParts * (D / 16) * 32 * 16;  // the query rows' operands, the same for all warps
   static constexpr size_t kBytes = kRing + kQBytes + 64 * sizeof(float) * kWarps;
+  static constexpr int kSumStride = D + 16;  // floats of a row of the warps' sums
+  static_assert(kWarps * kRowsT * kSumStride * 4 <= kRing, "the warps' sums take the ring's place");
 };
 
 template <int D, bool BF16, bool SEL>
@@ -121,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   const int sel_rt = (a.group + kRowsT - 1) / kRowsT, sel_tiles = (a.topk + kTile - 1) / kTile;
   if (SEL) {
     sel_rows = max64(min64(a.st.off[a.st.B], a.st.rows), 0);
-    total = sel_rows * a.c.hk * sel_rt * sel_tiles;
+    total = sel_rows * a.c.hk * sel_rt * (sel_tiles + kItemCost);
   } else {
     for (int b = lane; b < a.st.B; b += 32) {
       const int64_t w = weight_of(a, b);
@@ -138,13 +142,13 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   int64_t at = total * blockIdx.x / ctas;
   const int64_t stop = total * (blockIdx.x + 1) / ctas;
 
-  // the item that holds tile `at`: sequence b, item x of it, tile t of the item
+  // the item that holds place `at`: sequence b, item x of it, place t of the item
   int b = 0, x = 0, t = 0, per_b = 0;
   int64_t row = 0;
   Extent e{};
   if (SEL) {
-    const int64_t item = at / sel_tiles;
-    t = (int)(at - item * sel_tiles);
+    const int64_t item = at / (sel_tiles + kItemCost);
+    t = (int)(at - item * (sel_tiles + kItemCost));
     per_b = a.c.hk * sel_rt;
     row = item / per_b;
     x = (int)(item - row * per_b);
@@ -173,13 +177,15 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
     }
     e = extent_of(a, b);
     per_b = a.c.hk * e.row_tiles;
-    x = (int)(at / e.tiles);
-    t = (int)(at - (int64_t)x * e.tiles);
+    x = (int)(at / (e.tiles + kItemCost));
+    t = (int)(at - (int64_t)x * (e.tiles + kItemCost));
     at = total * blockIdx.x / ctas;
   }
 
   while (at < stop) {
-    const int t0 = t, t1 = (int)min64(e.tiles, t + (stop - at));
+    const int end = (int)min64(e.tiles + kItemCost, t + (stop - at));          // places [t, end) of the item
+    const int t0 = max(t - kItemCost, 0), t1 = max(end - kItemCost, 0);        // its tiles among them
+    if (t1 > t0) {  // else the item begins in the next stretch
     const int h = x / e.row_tiles, rr0 = (x - h * e.row_tiles) * kRowsT;  // key head, first of its query rows
     int64_t row0, first;
     int n, hi;
@@ -596,7 +602,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       }
     }
     __syncthreads();  // also: every warp is done with its ring
-    float* const sums = reinterpret_cast<float*>(smem);  // [warp][16][D]
+    // [warp][16 rows], 4 dims a piece: the pieces that the four lanes of a row store at a time stand side by side
+    float* const sums = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = g + 8 * i;
@@ -606,12 +613,12 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       // a row that saw nothing here has sums of zero, whatever its queries are
       const bool none = ref[i] == -INFINITY && l[i] == 0.f;
       const float f = ref[i] == -INFINITY ? 1.f : ex2(ref[i] - top);
-      float* to = sums + (warp * kRowsT + r) * D + 2 * NT * tig;
+      float* to = sums + (warp * kRowsT + r) * S::kSumStride + 4 * tig;
 #pragma unroll
       for (int k = 0; k < 2; ++k)
 #pragma unroll
         for (int n8 = 0; n8 < NT; n8 += 4)
-          *reinterpret_cast<float4*>(to + k * NT + n8) =
+          *reinterpret_cast<float4*>(to + 4 * (k * NT + n8)) =
               make_float4(none ? 0.f : o[n8][2 * i + k] * f, none ? 0.f : o[n8 + 1][2 * i + k] * f,
                           none ? 0.f : o[n8 + 2][2 * i + k] * f, none ? 0.f : o[n8 + 3][2 * i + k] * f);
     }
@@ -626,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         top = fmaxf(top, stats[w * 64 + r * 4]);
-        const float4 v = *reinterpret_cast<const float4*>(sums + (w * kRowsT + r) * D + c);
+        const float4 v = *reinterpret_cast<const float4*>(sums + (w * kRowsT + r) * S::kSumStride +
+                                                          4 * (c % (2 * NT)) + 4 * (c / (2 * NT)));
         s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
       }
 #pragma unroll
@@ -648,10 +656,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       }
     }
     if (!all && t0 == 0 && tid == 0)
-      *open = {row0, (int)blockIdx.x, h * a.group, rr0, valid, kv_parts(at - t0 + e.tiles, total, ctas) - (int)blockIdx.x};
+      *open = {row0, (int)blockIdx.x, h * a.group, rr0, valid, kv_parts(at - t + e.tiles + kItemCost, total, ctas) - (int)blockIdx.x};
     __syncthreads();  // the ring is free again
+    }
 
-    at += t1 - t0;
+    at += end - t;
     t = 0;
     if (++x == per_b && at < stop) {
       x = 0;
@@ -734,11 +743,11 @@ int line_ctas(int sms, const KvAttnArgs& a) {
   const int64_t per = a.is_bf16 ? 3 : 2;
   int64_t tiles;
   if (a.indices) {
-    tiles = a.st.rows * a.c.hk * ((a.group + kRowsT - 1) / kRowsT) * ((a.topk + kTile - 1) / kTile);
+    tiles = a.st.rows * a.c.hk * ((a.group + kRowsT - 1) / kRowsT) * ((a.topk + kTile - 1) / kTile + kItemCost);
   } else {
     const int64_t items = a.st.B + a.st.rows * a.group / kRowsT;
     const int64_t cap = (int64_t)a.st.width * a.c.ps;
-    tiles = items * a.c.hk * ((cap + kTile - 1) / kTile + 1);
+    tiles = items * a.c.hk * ((cap + kTile - 1) / kTile + 1 + kItemCost);
   }
   return (int)std::max<int64_t>(1, std::min<int64_t>(per * sms, tiles));
 }

@@ -26,6 +26,7 @@ constexpr int kTileB = kTok * D;             // bytes of an e4m3 tile
 constexpr int kSoft = 256, kConv = 128;      // threads: two softmax warpgroups, one of the converters
 constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWQk = kWTma + 1, kWPv = kWQk + 1;
 constexpr int kThreads = 32 * (kWPv + 1);
+constexpr int kItemCost = 8;   // what an item costs beside its tiles, in tiles
 constexpr float kLift = 2.f;  // a weight of the row's reference is 2^2 in fp16
 
 struct Meta {  // of a tile's 8 blocks
@@ -103,10 +104,10 @@ __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Seq& s, int r
   return tiles;
 }
 
-// Tiles of a sequence and one key head.  `wide`: the warp's lanes share one sequence's items; else a lane has its own.
+// Places in the line of a sequence and one key head: each item's tiles behind kItemCost.  `wide`: the warp's lanes share one sequence's items; else a lane has its own.
 __device__ __forceinline__ int64_t seq_tiles(const KvAttnArgs& a, const Seq& s, bool wide, int lane) {
   int64_t t = 0;
-  for (int rt = wide ? lane : 0; rt < s.row_tiles; rt += wide ? 32 : 1) t += tiles_of(a, s, rt);
+  for (int rt = wide ? lane : 0; rt < s.row_tiles; rt += wide ? 32 : 1) t += tiles_of(a, s, rt) + kItemCost;
   if (wide) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
@@ -119,7 +120,8 @@ struct Walk {
   int64_t at, stop, total, ctas;
   Item it;
   Seq s;
-  int t0, t1;  // tiles of the item in the stretch
+  int place, end;  // places [place, end) of the item in the stretch
+  int t0, t1;      // its tiles among them
   bool live;
 
   // tiles of 32 sequences, one a lane
@@ -166,7 +168,7 @@ struct Walk {
         in -= it.h * per;
         s = seq_of(a, it.b);
         for (int r0 = 0; r0 < s.row_tiles; r0 += 32) {  // the item: prefix over its sequence's row tiles
-          const int64_t v = r0 + lane < s.row_tiles ? tiles_of(a, s, r0 + lane) : 0;
+          const int64_t v = r0 + lane < s.row_tiles ? tiles_of(a, s, r0 + lane) + kItemCost : 0;
           int64_t pre = v;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -177,9 +179,9 @@ struct Walk {
           if (here) {
             const int k = __ffs(here) - 1;
             tiles_of(a, s, r0 + k, &it);
-            t0 = (int)(in - __shfl_sync(~0u, pre - v, k));
-            t1 = (int)min64(it.tiles, t0 + (stop - at));
+            cut((int)(in - __shfl_sync(~0u, pre - v, k)));
             live = true;
+            if (t1 <= t0) next(a);  // the item begins in the next stretch
             return;
           }
           in -= __shfl_sync(~0u, pre, 31);
@@ -190,29 +192,38 @@ struct Walk {
     }
   }
 
+  __device__ void cut(int from) {
+    place = from;
+    end = (int)min64(it.tiles + kItemCost, place + (stop - at));
+    t0 = max(place - kItemCost, 0);
+    t1 = max(end - kItemCost, 0);
+  }
+
+  // To the next item of which the stretch has tiles.
   __device__ void next(const KvAttnArgs& a) {
-    at += t1 - t0;
-    if (at >= stop) {
-      live = false;
-      return;
-    }
-    int rt = it.rt + 1;
-    if (rt == s.row_tiles) {
-      rt = 0;
-      if (++it.h == a.c.hk) {
-        it.h = 0;
-        do {
-          if (++it.b >= a.st.B) {
-            live = false;
-            return;
-          }
-          s = seq_of(a, it.b);
-        } while (s.row_tiles == 0);
+    do {
+      at += end - place;
+      if (at >= stop) {
+        live = false;
+        return;
       }
-    }
-    tiles_of(a, s, rt, &it);
-    t0 = 0;
-    t1 = (int)min64(it.tiles, stop - at);
+      int rt = it.rt + 1;
+      if (rt == s.row_tiles) {
+        rt = 0;
+        if (++it.h == a.c.hk) {
+          it.h = 0;
+          do {
+            if (++it.b >= a.st.B) {
+              live = false;
+              return;
+            }
+            s = seq_of(a, it.b);
+          } while (s.row_tiles == 0);
+        }
+      }
+      tiles_of(a, s, rt, &it);
+      cut(0);
+    } while (t1 <= t0);
   }
 };
 
@@ -778,7 +789,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (tid == 0 && !all && w.t0 == 0)
           args.line.open[blockIdx.x] = {it.row0, (int)blockIdx.x, it.h * a.group, it.rr0, it.valid,
-                                        kv_parts(w.at + it.tiles, w.total, w.ctas) - (int)blockIdx.x};
+                                        kv_parts(w.at - w.place + it.tiles + kItemCost, w.total, w.ctas) - (int)blockIdx.x};
       }
       n += nt;
     }
