@@ -579,3 +579,176 @@ def test_calls_without_rows_and_host_offsets():
     a, _ = P.kv_attention(q, cache, table, off, lens)
     b, _ = P.kv_attention(q, cache, table, [0, 2], [20], ws=P.Workspace("cuda"))
     assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------- calls large enough for the tcgen05 kernel
+# (more than 16 query rows for a key head on average, d = 128, bf16, and a table whose capacity promises enough work:
+# the sequences themselves may be short)
+
+WIDE = [
+    # lens, new, hq, hk, page, window, sinks, pad
+    ([1], [1], 17, 1, 16, 0, 0, 0),
+    ([0, 1, 128, 129], [5, 5, 5, 5], 5, 1, 64, 0, 0, 2),            # the first rows of the first two belong to none
+    ([127, 400], [7, 3], 48, 2, 48, 0, 0, 0),
+    ([700], [300], 6, 2, 16, 0, 0, 1),                              # 900 rows for a key head: 8 items
+    ([515, 260], [515, 260], 3, 1, 128, 0, 0, 0),                   # whole prompts
+    ([900, 333], [90, 40], 4, 1, 32, 200, 5, 0),
+    ([650], [400], 5, 1, 64, 1, 0, 0),                              # each row sees itself alone
+    ([650, 1], [400, 1], 2, 1, 16, 129, 300, 3),                    # more first tokens than the window has
+    ([1300], [20], 16, 1, 64, 100000, 4, 0),
+    ([40, 30], [40, 30], 1, 1, 16, 8, 3, 0),
+]
+
+
+def wide_step(lens, new, hq, hk, page, seed):
+    """make_step with room for 200,000 tokens a sequence, as a slice of a wider table."""
+    table, off, ln, pages = make_step(lens, new, page, seed)
+    wide = torch.full((len(lens), 200_000 // page + 7), -1, dtype=torch.int32, device="cuda")
+    wide[:, 3:3 + table.shape[1]] = table
+    return wide[:, 3:], off, ln, pages
+
+
+@pytest.mark.parametrize("scale", [None, -0.21, 0.0])
+@pytest.mark.parametrize("case", WIDE)
+def test_attention_of_many_rows_matches_the_definition(case, scale):
+    lens, new, hq, hk, page, window, sinks, pad = case
+    table, off, ln, pages = wide_step(lens, new, hq, hk, page, 1)
+    cache = make_cache(pages, hk, page, 128, 2)
+    q = make_q(sum(new) + pad, hq + 1, 128, "bf16", 3)[:, 1:]
+    ws = P.Workspace("cuda")
+
+    def run(out, lse):
+        P.kv_attention(q, cache, table, off, ln, scale=scale, window=window, sinks=sinks, lse=lse, out=out, ws=ws)
+        assert P.last_device_status(ws) == 0
+
+    check_attention(q, cache, table, off, ln, q.dtype, scale=scale, window=window, sinks=sinks, run=run)
+
+
+@pytest.mark.parametrize("new,group", [(5, 16), (90, 4)])
+def test_attention_of_many_rows_peaked_scores_and_scales_far_apart(new, group):
+    """Rows whose largest score comes late and high: the rows' reference has to follow it."""
+    lens, hk, page = [900, 300], 2, 32
+    table, off, ln, pages = wide_step(lens, [new, new], hk * group, hk, page, 4)
+    cache = make_cache(pages, hk, page, 128, 5)
+    cache.v_exp.copy_(torch.randint(-25, 6, cache.v_exp.shape, device="cuda", generator=gen(6)).to(torch.int8))
+    # scores grow along the sequence
+    tab = table.cpu().numpy()
+    for b, n in enumerate(lens):
+        for s in range(0, n, 16):
+            cache.k_exp[tab[b, s // page], :, s % page // 16] = -12 + s * 9 // n
+    q = make_q(2 * new, hk * group, 128, "bf16", 8, 4.0)
+    check_attention(q, cache, table, off, ln, q.dtype, scale=0.21)
+
+
+@pytest.mark.parametrize("new", [20, 90])
+def test_attention_of_many_rows_ignores_what_masked_places_hold(new):
+    """As for few rows: NaN payloads where no row, or only some rows, may look."""
+    lens, hk, page, group = [210], 1, 32, 4
+    table, off, ln, pages = wide_step(lens, [new], group, hk, page, 7)
+    cache = make_cache(pages, hk, page, 128, 8)
+    t = table.cpu().tolist()[0]
+    raw = [cache.k.view(torch.uint8), cache.v.view(torch.uint8)]
+    used = set(x for x in t if x >= 0)
+    for pg in range(pages):
+        if pg not in used:
+            for x in raw:
+                x[pg] = 0x7F
+            cache.k_exp[pg] = 127
+            cache.v_exp[pg] = 127
+    for x in raw:
+        x[t[6], :, 210 - 192:] = 0xFF
+    table[0, 2] = -1
+    q = make_q(new, group, 128, "bf16", 9)
+    check_attention(q, cache, table, off, ln, q.dtype)  # nothing but zeroed places
+    for x in raw:
+        x[t[6], :, 209 - 192] = 0x7F
+        x[t[1], :, 5] = 0xFF
+    check_attention(q, cache, table, off, ln, q.dtype)
+    check_attention(q, cache, table, off, ln, q.dtype, window=100, sinks=9)
+    for x in (raw[0][t[6]], raw[0][t[1]]):
+        x.fill_(0x38)
+    raw[1][t[6], :, 209 - 192] = 0x30
+    raw[1][t[6], :, 209 - 192, ::3] = 0x7F
+    check_attention(q, cache, table, off, ln, q.dtype, window=100, sinks=9)
+
+
+def test_attention_of_many_rows_a_row_of_non_finite_queries_touches_no_other():
+    table, off, ln, pages = wide_step([330, 20], [30, 20], 4, 1, 16, 1)
+    cache = make_cache(pages, 1, 16, 128, 2)
+    q = make_q(50, 4, 128, "bf16", 3)
+    clean, _ = P.kv_attention(q, cache, table, off, ln)
+    for bad in (float("nan"), float("inf")):
+        spoilt = q.clone()
+        spoilt[7, 2, 5] = bad
+        got, _ = P.kv_attention(spoilt, cache, table, off, ln)
+        assert torch.isnan(got[7, 2]).all()
+        keep = torch.ones((50, 4), dtype=torch.bool, device="cuda")
+        keep[7, 2] = False
+        assert torch.equal(got[keep], clean[keep])
+
+
+@pytest.mark.parametrize("window,sinks", [(0, 0), (700, 9)])
+def test_long_sequences_rows_together_and_alone(window, sinks):
+    """Lengths of thousands, where a call's items are cut into many parts: a group of rows in one call (tcgen05) and
+    each row in a call of its own (the few-row kernel) agree within their roundings, and so do ragged lengths."""
+    lens, n, hq, hk, page = [20_011, 1, 7_000, 130], 4, 16, 2, 64
+    table, off, ln, pages = make_step(lens, [n if x >= n else 1 for x in lens], page, 1)
+    cache = make_cache(pages, hk, page, 128, 2)
+    rows = int(off[-1])
+    q = make_q(rows, hq, 128, "bf16", 3)
+    q32 = q.float()
+    together, lse = P.kv_attention(q, cache, table, off, ln, window=window, sinks=sinks, lse=True)
+    exact, lse32 = P.kv_attention(q32, cache, table, off, ln, window=window, sinks=sinks, lse=True)
+    # A = sum p|v| / sum p <= 448 * 2^-4 of this cache's values; random signs keep the sum's error far below
+    assert (together.float() - exact).abs().max() <= 2.0 ** -7 * exact.abs().max() + 2.0 ** -8
+    assert (lse - lse32).abs().max() <= 2.0 ** -11 * lse32.abs().max()
+    of = off.tolist()
+    for b in range(len(lens)):
+        for r in range(of[b], of[b + 1]):
+            at = torch.tensor([lens[b] - of[b + 1] + r + 1], device="cuda")
+            one, one_lse = P.kv_attention(q32[r:r + 1], cache, table[b:b + 1], [0, 1], at, window=window, sinks=sinks,
+                                          lse=True)
+            assert (one[0] - exact[r]).abs().max() <= 2.0 ** -15 * exact[r].abs().max()
+            assert (one_lse[0] - lse32[r]).abs().max() <= 2.0 ** -18 * lse32[r].abs().max()
+
+
+def test_attention_of_many_rows_captured_and_on_two_streams():
+    hq, hk, page = 16, 1, 16
+    table, off, _, pages = wide_step([600, 600], [3, 3], hq, hk, page, 1)
+    cache = make_cache(pages, hk, page, 128, 2)
+    sets = []
+    for s in range(2):
+        q = make_q(6, hq, 128, "bf16", 3 + s)
+        ln = torch.tensor([300, 20], device="cuda")
+        P.kv_attention(q, cache, table, off, ln)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out, _ = P.kv_attention(q, cache, table, off, ln)
+        sets.append((q, ln, g, out))
+    sides = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for trial in range(3):
+        for s, (q, ln, _, _) in enumerate(sets):
+            ln.copy_(torch.tensor([600 - 37 * trial, 3 + 100 * s + trial]))
+            q.copy_(make_q(6, hq, 128, "bf16", 60 + trial + 7 * s))
+        torch.cuda.synchronize()
+        for (_, _, g, _), st in zip(sets, sides):
+            with torch.cuda.stream(st):
+                g.replay()
+        torch.cuda.synchronize()
+        for (q, ln, _, out), st in zip(sets, sides):
+            want, _ = P.kv_attention(q, cache, table, off, ln)
+            other, _ = P.kv_attention(q, cache, table, off, ln, stream=st)
+            torch.cuda.synchronize()
+            assert torch.equal(out, want) and torch.equal(other, want)
+
+
+@pytest.mark.parametrize("scale", [-0.4, 0.0])
+def test_attention_of_few_rows_takes_any_scale(scale):
+    table, off, ln, pages = make_step([300, 40], [2, 3], 32, 1)
+    for d, dtype in ((64, "f32"), (128, "bf16")):
+        cache = make_cache(pages, 2, 32, d, 2)
+        q = make_q(5, 6, d, dtype, 3)
+        check_attention(q, cache, table, off, ln, q.dtype, scale=scale)
+        idx = torch.randint(-1, 300, (5, 70), dtype=torch.int32, device="cuda", generator=gen(5))
+        check_attention(q, cache, table, off, ln, q.dtype, scale=scale, indices=idx)

@@ -1,5 +1,6 @@
 // kv_api.cu -- host side of the pivot_kv_* calls of include/pivot.h: argument checks and launches.  Nothing is
 // allocated and no call synchronises the host.
+#include <algorithm>
 #include <cmath>
 
 #include "kv.cuh"
@@ -73,9 +74,21 @@ bool payload_map(CUtensorMap* m, const void* base, int64_t rows) {
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Whether a call goes to the tcgen05 kernel.
+// Whether a call may go to the tcgen05 kernel.
 bool many_rows(int64_t rows, int B, int q_heads, int kv_heads, int d, pivot_dtype dt) {
   return dt == PIVOT_BF16 && d == 128 && rows * (q_heads / kv_heads) > 16 * (int64_t)B;
+}
+
+// Whether it pays there, by the most work that there can be, in tiles of 128 tokens by 16 query rows: that kernel
+// needs some 14 us more for its launches and first tiles, and takes a tile of 128 rows in the time of about 1.5 of 16.
+// Measured (16 against 128 rows an item, us): 1 sequence of 4000, 8 key heads of 64 rows (1024) 32 against 41, of 128
+// rows (2048) 43 against 41; 16 of 500, 4 heads of 24 rows (512) 26 against 29; 16 of 4000, 4 heads of 20 rows (4096)
+// 63 against 50; 16 of 32000, 2 heads of 64 rows (32000) 395 against 114.
+bool much_work(const pivot_kv_cache& c, const pivot_kv_step& s, int q_heads, int64_t window, int64_t sinks) {
+  const int64_t group = q_heads / c.kv_heads, cap = (int64_t)s.table_width * c.page_size;
+  int64_t seen = cap;
+  if (window > 0 && window < cap && sinks < cap) seen = std::min(cap, window + sinks + s.rows / s.B);
+  return (s.rows * group / 16 + s.B) * c.kv_heads * (seen / 128 + 1) >= 1536;
 }
 
 // Checks that the attention calls share, and the argument block they launch with.
@@ -177,7 +190,8 @@ pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step
   if (step->rows == 0) return PIVOT_OK;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (many_rows(step->rows, step->B, q_heads, cache->kv_heads, cache->d, dt)) {
+  if (many_rows(step->rows, step->B, q_heads, cache->kv_heads, cache->d, dt) &&
+      much_work(*cache, *step, q_heads, window, sinks)) {
     const int64_t slots = (int64_t)cache->num_pages * cache->kv_heads * cache->page_size;
     CUtensorMap kmap, vmap;
     if (!payload_map(&kmap, cache->k, slots) || !payload_map(&vmap, cache->v, slots))
