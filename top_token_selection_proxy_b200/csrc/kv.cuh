@@ -74,6 +74,7 @@ __device__ __forceinline__ int kv_parts(int64_t item_end, int64_t total, int64_t
 struct KvLine {
   int* status;
   const int* gate;  // null, or: run only where it is not 0
+  bool whole;       // items are not cut: each is one place of the line
   KvOpen* open;     // [ctas]
   float* part;      // [ctas][2][kv_part_floats]: of an item that the stretch ends, of one that it begins
 };

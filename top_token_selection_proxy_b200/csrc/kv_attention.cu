@@ -30,6 +30,7 @@ constexpr int kRowsT = 16;              // query rows of an item
 constexpr int kWTok = 32;               // tokens a warp takes at a time (two blocks)
 constexpr int kTile = kWTok * kWarps;   // tokens of a tile
 constexpr int kItemCost = 4;            // what an item costs beside its tiles, in tiles
+constexpr int kWholeTiles = 2;          // items of so few tiles are not cut
 constexpr float kLift = 2.f;            // a weight of the row's reference is 2^2 in fp16
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -85,10 +86,13 @@ __device__ __forceinline__ Extent extent_of(const KvAttnArgs& a, int b) {
   return e;
 }
 
-__device__ __forceinline__ int64_t weight_of(const KvAttnArgs& a, int b) {
+// Places of an item in the line.
+__device__ __forceinline__ int places(const KvLine& line, int tiles) { return line.whole ? 1 : tiles + kItemCost; }
+
+__device__ __forceinline__ int64_t weight_of(const KvAttnArgs& a, const KvLine& line, int b) {
   if (b >= a.st.B) return 0;
   const Extent e = extent_of(a, b);
-  return (int64_t)a.c.hk * e.row_tiles * (e.tiles + kItemCost);
+  return (int64_t)a.c.hk * e.row_tiles * places(line, e.tiles);
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -125,10 +129,10 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   const int sel_rt = (a.group + kRowsT - 1) / kRowsT, sel_tiles = (a.topk + kTile - 1) / kTile;
   if (SEL) {
     sel_rows = max64(min64(a.st.off[a.st.B], a.st.rows), 0);
-    total = sel_rows * a.c.hk * sel_rt * (sel_tiles + kItemCost);
+    total = sel_rows * a.c.hk * sel_rt * places(line, sel_tiles);
   } else {
     for (int b = lane; b < a.st.B; b += 32) {
-      const int64_t w = weight_of(a, b);
+      const int64_t w = weight_of(a, line, b);
       if (b < 32) w_first = w;
       total += w;
     }
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   }
   const int64_t ctas = min64(gridDim.x, total);
   KvOpen* const open = line.open + blockIdx.x;
-  if (tid == 0) open->open = 0;
+  if (tid == 0 && !line.whole) open->open = 0;
   if (blockIdx.x >= ctas) return;
   int64_t at = total * blockIdx.x / ctas;
   const int64_t stop = total * (blockIdx.x + 1) / ctas;
@@ -147,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   int64_t row = 0;
   Extent e{};
   if (SEL) {
-    const int64_t item = at / (sel_tiles + kItemCost);
-    t = (int)(at - item * (sel_tiles + kItemCost));
+    const int64_t item = at / places(line, sel_tiles);
+    t = (int)(at - item * places(line, sel_tiles));
     per_b = a.c.hk * sel_rt;
     row = item / per_b;
     x = (int)(item - row * per_b);
@@ -159,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
     int64_t run = 0;
     for (int b0 = 0;; b0 += 32) {
       if (b0 >= a.st.B) return;  // only where the lengths changed under the call
-      const int64_t w = b0 ? weight_of(a, b0 + lane) : w_first;
+      const int64_t w = b0 ? weight_of(a, line, b0 + lane) : w_first;
       int64_t inc = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -177,14 +181,15 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
     }
     e = extent_of(a, b);
     per_b = a.c.hk * e.row_tiles;
-    x = (int)(at / (e.tiles + kItemCost));
-    t = (int)(at - (int64_t)x * (e.tiles + kItemCost));
+    x = (int)(at / places(line, e.tiles));
+    t = (int)(at - (int64_t)x * places(line, e.tiles));
     at = total * blockIdx.x / ctas;
   }
 
   while (at < stop) {
-    const int end = (int)min64(e.tiles + kItemCost, t + (stop - at));          // places [t, end) of the item
-    const int t0 = max(t - kItemCost, 0), t1 = max(end - kItemCost, 0);        // its tiles among them
+    const int end = (int)min64(places(line, e.tiles), t + (stop - at));  // places [t, end) of the item
+    const int t0 = line.whole ? 0 : max(t - kItemCost, 0);               // its tiles among them
+    const int t1 = line.whole ? e.tiles : max(end - kItemCost, 0);
     if (t1 > t0) {  // else the item begins in the next stretch
     const int h = x / e.row_tiles, rr0 = (x - h * e.row_tiles) * kRowsT;  // key head, first of its query rows
     int64_t row0, first;
@@ -738,18 +743,26 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   if (a.lse && lane == 0) a.lse[row * a.hq + j] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
 }
 
-// CTAs of the line: as many as the device holds at once, but no more than there can be tiles.
+// The most items that a call can have, and tiles of each.
+int64_t most_items(const KvAttnArgs& a) {
+  return a.indices ? a.st.rows * a.c.hk * ((a.group + kRowsT - 1) / kRowsT)
+                   : (a.st.B + a.st.rows * a.group / kRowsT) * (int64_t)a.c.hk;
+}
+int64_t most_tiles(const KvAttnArgs& a) {
+  if (a.indices) return (a.topk + kTile - 1) / kTile;
+  const int64_t cap = (int64_t)a.st.width * a.c.ps;
+  return (cap + kTile - 1) / kTile + (a.window > 0 ? 1 : 0);
+}
+
+// Items of one or two tiles are not cut: a CTA takes whole ones, and no launch joins parts (a list of 97 for 8 rows:
+// 6.6 us in a graph against 7.6).  With more the cut pays (512 tokens, 8 key heads, in 5 tiles: 15.3 us whole, 14.4 cut).
+bool whole_items(const KvAttnArgs& a) { return most_tiles(a) <= kWholeTiles; }
+
+// CTAs of the line: as many as the device holds at once, but no more than there can be places.
 int line_ctas(int sms, const KvAttnArgs& a) {
   const int64_t per = a.is_bf16 ? 3 : 2;
-  int64_t tiles;
-  if (a.indices) {
-    tiles = a.st.rows * a.c.hk * ((a.group + kRowsT - 1) / kRowsT) * ((a.topk + kTile - 1) / kTile + kItemCost);
-  } else {
-    const int64_t items = a.st.B + a.st.rows * a.group / kRowsT;
-    const int64_t cap = (int64_t)a.st.width * a.c.ps;
-    tiles = items * a.c.hk * ((cap + kTile - 1) / kTile + 1 + kItemCost);
-  }
-  return (int)std::max<int64_t>(1, std::min<int64_t>(per * sms, tiles));
+  const int64_t places = most_items(a) * (whole_items(a) ? 1 : most_tiles(a) + kItemCost);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(per * sms, places));
 }
 
 KvLine carve_line(void* ws, int ctas) {
@@ -768,10 +781,9 @@ cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaS
   if (e != cudaSuccess) return e;
   kv_attn_kernel<D, BF16, SEL><<<ctas, kThreads, Sh::kBytes, s>>>(a, line);
   e = cudaGetLastError();
-  if (e != cudaSuccess || ctas == 1) return e;
+  if (e != cudaSuccess || ctas == 1 || line.whole) return e;
   // Few items cut into many parts: all warps of a block for a row; else a warp.
-  const int64_t items = a.indices ? a.st.rows * a.c.hk : (a.st.B + a.st.rows * a.group / kRowsT) * (int64_t)a.c.hk;
-  return launch_kv_merge(a, line, ctas, kRowsT, ctas > 8 * items, kLift, s);
+  return launch_kv_merge(a, line, ctas, kRowsT, ctas > 8 * most_items(a), kLift, s);
 }
 
 }  // namespace
@@ -803,6 +815,7 @@ cudaError_t launch_kv_attn(const KvAttnArgs& a, int sms, void* ws, const int* ga
   const int ctas = line_ctas(sms, a);
   KvLine line = carve_line(ws, ctas);
   line.gate = gate;
+  line.whole = whole_items(a);
   const bool sel = a.indices != nullptr;
   if (a.c.d == 128) {
     if (a.is_bf16) return sel ? launch_line<128, true, true>(a, ctas, line, s) : launch_line<128, true, false>(a, ctas, line, s);
