@@ -95,10 +95,18 @@ __device__ __forceinline__ int64_t weight_of(const KvAttnArgs& a, const KvLine& 
   return (int64_t)a.c.hk * e.row_tiles * places(line, e.tiles);
 }
 
+// Where a CTA stands in the line: kept in shared memory while it works on an item, for the loop needs the registers.
+struct Place {
+  int64_t at, stop, total, ctas, row0, row;
+  int t0, t1, t, end, rr0, h, valid, x, b, per_b;
+  Extent e;
+};
+
 // ---------------------------------------------------------------- the kernel
 template <int D, bool BF16, bool SEL>
 struct Shape {
-  static constexpr int kStages = D == 128 ? 2 : 4;
+  static constexpr int kCtas = !BF16 || (D == 128 && !SEL) ? 2 : 3;  // an SM holds
+  static constexpr int kStages = D == 64 ? 4 : SEL && BF16 ? 2 : 3;
   static constexpr int kKPieces = 4 * (D / 64);         // 16-byte pieces of keys a lane holds of 32 tokens
   static constexpr int kVBytes = D / 8;                 // bytes of a value a lane holds
   static constexpr int kStageBytes = 32 * (kKPieces * 16 + 8 * kVBytes + 4);  // a warp's; 4: the tokens' scales
@@ -111,10 +119,11 @@ struct Shape {
 };
 
 template <int D, bool BF16, bool SEL>
-__global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const KvAttnArgs a, const KvLine line) {
+__global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_kernel(const KvAttnArgs a, const KvLine line) {
   using S = Shape<D, BF16, SEL>;
   constexpr int NK = D / 16, NT = D / 8, kStages = S::kStages;
   extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ Place place;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, tig = lane % 4;
   float* const stats = reinterpret_cast<float*>(smem + S::kRing + S::kQBytes);  // [warp][16 rows][m', m, l]
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
@@ -139,12 +148,12 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(~0u, total, o);
   }
-  const int64_t ctas = min64(gridDim.x, total);
+  int64_t ctas = min64(gridDim.x, total);
   KvOpen* const open = line.open + blockIdx.x;
   if (tid == 0 && !line.whole) open->open = 0;
   if (blockIdx.x >= ctas) return;
   int64_t at = total * blockIdx.x / ctas;
-  const int64_t stop = total * (blockIdx.x + 1) / ctas;
+  int64_t stop = total * (blockIdx.x + 1) / ctas;
 
   // the item that holds place `at`: sequence b, item x of it, place t of the item
   int b = 0, x = 0, t = 0, per_b = 0;
@@ -187,11 +196,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
   }
 
   while (at < stop) {
-    const int end = (int)min64(places(line, e.tiles), t + (stop - at));  // places [t, end) of the item
-    const int t0 = line.whole ? 0 : max(t - kItemCost, 0);               // its tiles among them
-    const int t1 = line.whole ? e.tiles : max(end - kItemCost, 0);
+    int end = (int)min64(places(line, e.tiles), t + (stop - at));  // places [t, end) of the item
+    int t0 = line.whole ? 0 : max(t - kItemCost, 0);               // its tiles among them
+    int t1 = line.whole ? e.tiles : max(end - kItemCost, 0);
     if (t1 > t0) {  // else the item begins in the next stretch
-    const int h = x / e.row_tiles, rr0 = (x - h * e.row_tiles) * kRowsT;  // key head, first of its query rows
+    int h = x / e.row_tiles, rr0 = (x - h * e.row_tiles) * kRowsT;  // key head, first of its query rows
     int64_t row0, first;
     int n, hi;
     if (SEL) {
@@ -205,10 +214,22 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       first = e.first;
       hi = e.hi;
     }
-    const int valid = (int)min64(kRowsT, (int64_t)n * a.group - rr0);
-    // positions of this lane's two rows, and of the item's first and last; far below zero they see nothing
+    int valid = (int)min64(kRowsT, (int64_t)n * a.group - rr0);
+    if (tid == 0) place = {at, stop, total, ctas, row0, row, t0, t1, t, end, rr0, h, valid, x, b, per_b, e};
+    // What this lane's two rows see, and what all rows of the item do, as positions that fit 32 bits: up to sees_upto,
+    // from sees_from on or among the first `sinks`.  (64-bit positions in the loop would cost it its registers.)
+    auto small = [](int64_t v) { return (int)min64(max64(v, -1), 0x7FFFFFF0); };
+    const bool windowed = !SEL && a.window > 0;
     const int64_t p_lo = first + rr0 / a.group, p_hi = first + (rr0 + valid - 1) / a.group;
-    const int64_t pr[2] = {first + (rr0 + min(g, valid - 1)) / a.group, first + (rr0 + min(g + 8, valid - 1)) / a.group};
+    int sees_upto[2], sees_from[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int64_t p = first + (rr0 + min(g + 8 * i, valid - 1)) / a.group;
+      sees_upto[i] = small(min64(p, hi));
+      sees_from[i] = windowed ? max(small(p - a.window + 1), 0) : 0;
+    }
+    const int whole_upto = small(min64(p_lo, hi)), whole_from = windowed ? max(small(p_hi - a.window + 1), 0) : 0;
+    const int sinks = windowed ? small(a.sinks) : 0;
 
     // q: this lane's operands, scaled by a power of two so that the row's largest lies in [2^14, 2^15): one fp16 holds
     // a bf16's 8 bits (down to 2^-31 of the largest), three hold an fp32's 24.
@@ -292,10 +313,9 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       tb = t0;
     }
     const int steps = ahead + max(tb - w0, 0);
+    const int gap = w0 - ahead + (SEL ? 0 : e.lo_tile - e.sink_tiles);  // places in the line to tiles, past the first tokens'
     auto base_of = [&](int step) {  // first of this warp's tokens (positions, or places in the list)
-      const int tt = step < ahead ? t0 + step : w0 + step - ahead;
-      const int tile = SEL || tt < e.sink_tiles ? tt : e.lo_tile + tt - e.sink_tiles;
-      return tile * kTile + warp * kWTok;
+      return (step < ahead ? t0 + step : gap + step) * kTile + warp * kWTok;
     };
 
     // Look-ups run ahead of the copies, a step between each and the next: list entries (selected), then pages, then the
@@ -411,8 +431,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 
       // mask
       const bool whole = __all_sync(~0u, scales[lane] != 0) &&
-                         (SEL || (base + kWTok - 1 <= min64(p_lo, hi) &&
-                                  (a.window <= 0 || base > p_hi - a.window || base + kWTok <= a.sinks)));
+                         (SEL || (base + kWTok - 1 <= whole_upto && (base >= whole_from || base + kWTok <= sinks)));
       uint32_t te[4][2];  // scales of the two tokens that this lane holds in each tile
       if (SEL) {
 #pragma unroll
@@ -434,8 +453,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
             const int s = base + 8 * j + 2 * tig + k;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const bool seen = te[j][k] && (SEL || (s <= hi && s <= pr[i] &&
-                                                     (a.window <= 0 || s > pr[i] - a.window || s < a.sinks)));
+              const bool seen = te[j][k] && (SEL || (s <= sees_upto[i] && (s >= sees_from[i] || s < sinks)));
               if (!seen) z[j][2 * i + k] = -INFINITY;
             }
           }
@@ -540,7 +558,11 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
         odd = __any_sync(~0u, odd);
       }
       auto product = [&](auto by_row, int only) {  // by_row: of row `only` alone
-        const int64_t p = first + (rr0 + max(only, 0)) / a.group;
+        int upto = 0, from = 0;  // what that row sees: its lanes hold it
+        if (by_row) {
+          upto = __shfl_sync(~0u, only < 8 ? sees_upto[0] : sees_upto[1], only % 8 * 4);
+          from = __shfl_sync(~0u, only < 8 ? sees_from[0] : sees_from[1], only % 8 * 4);
+        }
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t w[4][VW];
@@ -549,7 +571,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int s = base + 16 * u + 8 * (j / 2) + 2 * tig + j % 2;
-              if (!(s <= p && (a.window <= 0 || s > p - a.window || s < a.sinks))) {
+              if (!(s <= upto && (s >= from || s < sinks))) {
 #pragma unroll
                 for (int k = 0; k < VW; ++k) w[j][k] = 0u;
               }
@@ -578,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
         }
       };
       if (!odd) {
-        product(std::false_type{}, -1);
+        product(std::false_type{}, 0);
       } else {
 #pragma unroll 1
         for (int only = 0; only < valid; ++only) product(std::true_type{}, only);
@@ -607,6 +629,13 @@ __global__ void __launch_bounds__(kThreads, BF16 ? 3 : 2) kv_attn_kernel(const K
       }
     }
     __syncthreads();  // also: every warp is done with its ring
+    {
+      const volatile Place& p = place;
+      at = p.at, stop = p.stop, total = p.total, ctas = p.ctas, row0 = p.row0, row = p.row;
+      t0 = p.t0, t1 = p.t1, t = p.t, end = p.end, rr0 = p.rr0, h = p.h, valid = p.valid, x = p.x, b = p.b, per_b = p.per_b;
+      e.first = p.e.first, e.hi = p.e.hi, e.sink_tiles = p.e.sink_tiles, e.lo_tile = p.e.lo_tile, e.tiles = p.e.tiles;
+      e.row_tiles = p.e.row_tiles;
+    }
     // [warp][16 rows], 4 dims a piece: the pieces that the four lanes of a row store at a time stand side by side
     float* const sums = reinterpret_cast<float*>(smem);
 #pragma unroll
@@ -760,7 +789,7 @@ bool whole_items(const KvAttnArgs& a) { return most_tiles(a) <= kWholeTiles; }
 
 // CTAs of the line: as many as the device holds at once, but no more than there can be places.
 int line_ctas(int sms, const KvAttnArgs& a) {
-  const int64_t per = a.is_bf16 ? 3 : 2;
+  const int64_t per = !a.is_bf16 || (a.c.d == 128 && !a.indices) ? 2 : 3;
   const int64_t places = most_items(a) * (whole_items(a) ? 1 : most_tiles(a) + kItemCost);
   return (int)std::max<int64_t>(1, std::min<int64_t>(per * sms, places));
 }
@@ -789,7 +818,7 @@ cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaS
 }  // namespace
 
 size_t kv_attn_workspace(int sms, int d) {
-  return 256 + (size_t)3 * sms * (sizeof(KvOpen) + 2 * kv_part_floats(kRowsT, d) * sizeof(float));
+  return 256 + (size_t)4 * sms * (sizeof(KvOpen) + 2 * kv_part_floats(kRowsT, d) * sizeof(float));
 }
 
 cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, bool many, float lift,
