@@ -712,6 +712,23 @@ def test_long_sequences_rows_together_and_alone(window, sinks):
             assert (one_lse[0] - lse32[r]).abs().max() <= 2.0 ** -18 * lse32[r].abs().max()
 
 
+@pytest.mark.parametrize("B,length,new,hq,hk,window", [
+    (4, 8000, 4, 64, 8, 0),      # items of 32 rows: warps without rows beside one that has them
+    (2, 8000, 4, 40, 8, 0),      # of 20
+    (1, 9000, 8, 128, 8, 0),     # of 128
+    (3, 2000, 300, 32, 2, 256),  # a window; several items a sequence, the last of fewer rows
+])
+def test_attention_of_many_rows_over_many_tiles_is_right_every_time(B, length, new, hq, hk, window):
+    table, off, ln, pages = make_step([length] * B, [new] * B, 64, 1)
+    cache = make_cache(pages, hk, 64, 128, 2)
+    q = make_q(B * new, hq, 128, "bf16", 3)
+    check_attention(q, cache, table, off, ln, q.dtype, window=window)
+    want = P.kv_attention(q, cache, table, off, ln, window=window, lse=True)
+    for _ in range(20):
+        got = P.kv_attention(q, cache, table, off, ln, window=window, lse=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_attention_of_many_rows_captured_and_on_two_streams():
     hq, hk, page = 16, 1, 16
     table, off, _, pages = wide_step([600, 600], [3, 3], hq, hk, page, 1)

@@ -79,7 +79,7 @@ struct KvLine {
   float* part;      // [ctas][2][kv_part_floats]: of an item that the stretch ends, of one that it begins
 };
 
-// Partial result of an item of `rows` query rows: sums [rows][d], then (m', m, l, 0) of each row.
+// Partial result of an item of `rows` query rows: sums [rows][d], then (reference, l, 0, 0) of each row.
 __host__ __device__ constexpr size_t kv_part_floats(int rows, int d) { return (size_t)rows * (d + 4); }
 
 // Lets a kernel use its dynamic shared memory, once on each device.

@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ Place place;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, tig = lane % 4;
-  float* const stats = reinterpret_cast<float*>(smem + S::kRing + S::kQBytes);  // [warp][16 rows][m', m, l]
+  float* const stats = reinterpret_cast<float*>(smem + S::kRing + S::kQBytes);  // [warp][16 rows][u, l]
   const uint32_t ring = smem_u32(smem) + warp * kStages * S::kStageBytes;
   if (line.gate) {
     if (*line.gate == 0) return;
@@ -686,7 +686,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_
         }
       } else {
         *reinterpret_cast<float4*>(part + r * D + c) = s;
-        if (c == 0) *reinterpret_cast<float4*>(part + kRowsT * D + r * 4) = make_float4(top, top, lt, 0.f);
+        if (c == 0) *reinterpret_cast<float4*>(part + kRowsT * D + r * 4) = make_float4(top, lt, 0.f, 0.f);
       }
     }
     if (!all && t0 == 0 && tid == 0)
@@ -730,27 +730,20 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     return line.part + ((int64_t)(op.stretch + i) * 2 + (i == 0)) * kv_part_floats(rows, D);
   };
   const int64_t stat_at = (int64_t)rows * D + (int64_t)min(r, rows - 1) * 4;
-  float mp = -INFINITY, m = -INFINITY;
-  for (int i = lane; i <= more; i += 32) {
-    const float4 s = *reinterpret_cast<const float4*>(part_of(i) + stat_at);
-    mp = fmaxf(mp, s.x);
-    m = fmaxf(m, s.y);
-  }
+  float u = -INFINITY;  // the largest reference
+  for (int i = lane; i <= more; i += 32) u = fmaxf(u, part_of(i)[stat_at]);
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    mp = fmaxf(mp, __shfl_xor_sync(~0u, mp, o));
-    m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-  }
+  for (int o = 16; o; o >>= 1) u = fmaxf(u, __shfl_xor_sync(~0u, u, o));
   float l = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   const bool mine = lane * 4 < D && r < op.valid;
 #pragma unroll 4
   for (int i = sub; i <= more; i += per_row) {
     const float* p = part_of(i);
-    const float4 s = *reinterpret_cast<const float4*>(p + stat_at);
+    const float2 s = *reinterpret_cast<const float2*>(p + stat_at);
     const float4 v = mine ? *reinterpret_cast<const float4*>(p + r * D + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-    l += s.y == -INFINITY ? s.z : s.z * ex2(s.y - m);
-    const float f = s.x == -INFINITY ? (s.z == 0.f ? 0.f : 1.f) : ex2(s.x - mp);
+    const float f = s.x == -INFINITY ? (s.y == 0.f ? 0.f : 1.f) : ex2(s.x - u);  // no reference: nothing, or NaN of a score
+    l = fmaf(s.y, f, l);
     if (f != 0.f) acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
   }
   if (per_row > 1) {
@@ -767,9 +760,9 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
   const int64_t row = op.row0 + (op.rr0 + r) / a.group;
   if (r >= op.valid || row >= a.st.rows) return;
   const int j = op.head0 + (op.rr0 + r) % a.group;
-  const float f = l == 0.f ? 0.f : ex2(mp - m - lift) / l;
+  const float f = l == 0.f ? 0.f : ex2(-lift) / l;
   if (mine) kv_store4(a, (row * a.hq + j) * (int64_t)D + lane * 4, acc.x * f, acc.y * f, acc.z * f, acc.w * f, BF16);
-  if (a.lse && lane == 0) a.lse[row * a.hq + j] = l == 0.f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+  if (a.lse && lane == 0) a.lse[row * a.hq + j] = l == 0.f ? -INFINITY : 0.6931471805599453f * (u + log2f(l));
 }
 
 // The most items that a call can have, and tiles of each.

@@ -234,8 +234,8 @@ struct Tail {
   Meta meta[kMeta];
   Walk walk[kWPv + 1];  // one for each warp: in registers it would crowd out the softmax
   float unit[M];
-  float ref[M];          // m' of each row
-  float stats[2][M][2];  // (m, l) of each half's tiles
+  float ref[M];          // each row's reference, settled tile after tile
+  float stats[2][M][2];  // reference and l of each half's tiles
 };
 
 constexpr int kOffQ = 0, kOffK = 2 * M * D, kOffV = kOffK + kKS * kTileB, kOffH = kOffV + kVS * kTileB,
@@ -607,19 +607,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         };
         // what a block's scores are multiplied by; never 0: a hidden score, -inf, times it stays -inf
         auto factor = [&](float ks) { return fmaxf(unit * ks, 1e-37f); };
-        // One pass: weights relative to the reference u that is known when the tile begins.  It may lag behind the
-        // largest score as long as fp16 holds the weights (32 of them sum to 2^15 at most); a row for which it does not,
+        // One pass: weights relative to the reference u that this half settled on last.  It may lag behind the largest
+        // score as long as fp16 holds the weights (32 of them sum to 2^15 at most); a row for which it does not,
         // or that has none yet, takes a new one from the scores in hand, and what it weighed before is scaled down.
         // After an item's first tiles that is rare.  (The loops are not unrolled, and masked tiles have code of their
         // own: the code then stays in the instruction cache.  Unrolled it ran at half the speed, and in one copy the
         // compiler masks every tile.)
-        if (k >= 2) {
-          const float known = T.ref[r];  // of the tile before, or still of the one before that: settled at the end
-          if (known > u) {
-            l *= ex2(u - known);
-            u = known;
-          }
-        }
         auto scale_weights = [&](int columns, float f) {  // this tile's first ones
           const __half2 fh = __float2half2_rn(f);
           tmem_wait_st();
@@ -701,6 +694,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (idle) {
           tc_fence_before();
           mbar_arrive(&T.sc[s]);
+          // As the other warps: else it could count for two tiles in one phase of pf, before their weights are there.
+          if (k >= 2) ok = wait(&T.od[s], (mine - 1) & 1);
         } else if (whole) {
           weigh(std::true_type{});
         } else {
@@ -784,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (all) {
             if (a.lse) a.lse[row * a.hq + j] = none ? -INFINITY : 0.6931471805599453f * (ref - kLift + log2f(lt));
           } else {
-            *reinterpret_cast<float4*>(part + M * D + r * 4) = make_float4(ref, ref, lt * ex2(-kLift), 0.f);
+            *reinterpret_cast<float4*>(part + M * D + r * 4) = make_float4(ref, lt * ex2(-kLift), 0.f, 0.f);
           }
         }
         if (tid == 0 && !all && w.t0 == 0)
