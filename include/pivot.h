@@ -354,7 +354,8 @@ typedef struct {
  * or (2i, 2i + 1) with `interleaved`, become (x1 cos - x2 sin, x2 cos + x1 sin).  rot is a multiple of 16, at
  * most d (0: no rotation, cos and sin NULL); n_pos >= table_width * page_size; cos and sin 16-byte aligned.
  * q [rows, q_heads, d] (optional) is rotated the same way into q_out [rows, q_heads, d] (dt), which may be q
- * itself (then with the same stride).
+ * itself (then with the same stride) and else shares no element with it.  Rows of positions behind the table's
+ * width keep their q_out as it was.
  *
  * The scale of a block whose first token of the sequence is new: the least e in [PIVOT_KV_EXP_MIN,
  * PIVOT_KV_EXP_MAX] with |y| <= 448 * 2^e for the finite values y of its new tokens and head.  A block that
@@ -378,8 +379,10 @@ PIVOT_API pivot_status pivot_kv_append(const pivot_kv_cache *cache, const pivot_
  * that sees nothing gives zeros and lse -inf.  What absent or masked positions hold, NaN included, changes nothing.
  * Scores, softmax statistics and output sums are fp32.  bf16: the weights p enter the output product with 8 bits
  * or more; fp32: with 21 or more.
+ * The same call gives the same bits every time.  out must not overlap q.
  * ws: pivot_kv_workspace_size bytes on the current device (256-byte aligned; 0: the call would be refused), with
- * topk 0 for pivot_kv_attention. */
+ * topk 0 for pivot_kv_attention.  pivot_last_device_status reads it.  None of these calls records the events of
+ * pivot_set_profile_events. */
 PIVOT_API size_t pivot_kv_workspace_size(int64_t rows, int B, int q_heads, int kv_heads, int d, int topk,
                                          pivot_dtype dt);
 PIVOT_API pivot_status pivot_kv_attention(const pivot_kv_cache *cache, const pivot_kv_step *step, const void *q,

@@ -566,6 +566,20 @@ def test_results_do_not_change_from_call_to_call():
         assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
+def test_arguments_past_64_bits_and_a_workspace_elsewhere():
+    table, off, ln, pages = make_step([200], [3], 32, 1)
+    cache = make_cache(pages, 1, 32, 64, 2)
+    q = make_q(3, 4, 64, "bf16", 3)
+    for far in (2 ** 63 - 1, 2 ** 64 + 1):
+        for window in (far, 5):  # either way every row sees all
+            check_attention(q, cache, table, off, ln, q.dtype, run=lambda out, lse: P.kv_attention(
+                q, cache, table, off, ln, window=window, sinks=far, out=out, lse=lse))
+    with pytest.raises(ValueError, match="workspace"):
+        P.kv_attention(q, cache, table, off, ln, ws=P.Workspace("cpu"))
+    with pytest.raises(P.PivotError):
+        P.kv_attention(q, cache, table, off, ln, out=q)
+
+
 def test_calls_without_rows_and_host_offsets():
     cache = make_cache(3, 2, 16, 64, 1)
     table = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda")

@@ -95,6 +95,18 @@ def test_attention_refusals(lib, call):
     assert call(lib, cache(), step(rows=0)) == 0
 
 
+@pytest.mark.parametrize("call", [attend, select])
+def test_attention_refuses_a_scale_past_fp32_and_outputs_over_the_queries(lib, call):
+    far = PTR + 3 * 1024 * 2
+    assert call(lib, cache(), step(rows=0), out=far, scale=3e38) == 1   # times log2(e) it is infinite
+    assert call(lib, cache(), step(rows=0), out=far, scale=2e38) == 0
+    for at in (0, 16, 3 * 1024 * 2 - 16):                               # 3 rows of 1024 bf16 values
+        assert call(lib, cache(), step(), q=PTR, out=PTR + at) == 1, at
+        assert call(lib, cache(), step(), q=PTR + at, out=PTR) == 1, at
+    # rows further apart: the last one counts whole
+    assert call(lib, cache(), step(), q=PTR, qs=2048, out=PTR + (2 * 2048 + 1024) * 2 - 16) == 1
+
+
 def test_window_and_list_refusals(lib):
     assert attend(lib, cache(), step(), window=-1) == 1
     assert attend(lib, cache(), step(), sinks=-1) == 1

@@ -654,6 +654,7 @@ def _kv_rows(name, t, heads, cache, dtype=None):
     return r if shape[0] > 1 else max(r, shape[1] * shape[2])
 
 
+_FAR = 1 << 62  # more tokens than there can be
 _KV_TYPES = {torch.bfloat16: BF16, torch.float32: F32}
 
 
@@ -681,9 +682,9 @@ def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None,
     row_offsets[b] .. row_offsets[b+1]-1, the last of its lens[b] tokens (this step's included), and its
     position s lies in page block_table[b, s // page_size].  row_offsets [B+1] and lens [B]: int64 CUDA
     tensors, DeviceOffsets, or host values (copied on every call).  cos, sin [positions, rot / 2] fp32
-    rotate the first rot dims of k, and of q [rows, heads, d] into q_out (a new tensor unless given; q
+    (positions >= width * page_size) rotate the first rot dims of k, and of q [rows, heads, d] into q_out (a new tensor unless given; q
     itself is allowed): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no
-    token leave cache and q_out as they were."""
+    token, or lie behind the table's width, leave cache and q_out as they were."""
     other = _kv_elsewhere(cache, stream)
     if other is not None:
         with torch.cuda.stream(other):
@@ -741,7 +742,12 @@ def _kv_scratch(rows, B, heads, cache, topk, dt, ws, where):
         if len(_kv_sizes) > 4096:
             _kv_sizes.clear()
         _kv_sizes[key] = n
-    return torch.empty(n, dtype=torch.uint8, device=cache.device) if ws is None else ws.get(n)
+    if ws is None:
+        return torch.empty(n, dtype=torch.uint8, device=cache.device)
+    buf = ws.get(n)
+    if buf.device != cache.device:
+        raise ValueError(f"the workspace is on {buf.device}, the cache on {cache.device}")
+    return buf
 
 
 def _kv_results(q, cache, out, lse):
@@ -766,7 +772,8 @@ def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Op
 
     q [rows, heads, d] (bf16 or fp32), heads a multiple of the cache's; the step as kv_append takes it,
     after it.  The row at position p sees the positions s <= p; with ``window`` only s > p - window, and the
-    first ``sinks``.  ``scale`` defaults to d ** -0.5.  ``lse``: False, True, or an fp32 [rows, heads] tensor
+    first ``sinks``.  ``scale`` defaults to d ** -0.5.  ``out`` must not share memory with q.  ``ws``: scratch kept
+    between calls, which must then be ordered (last_device_status reads it); else each call has its own.  ``lse``: False, True, or an fp32 [rows, heads] tensor
     that receives ln sum exp(scale q.k).  Rows that see nothing give zeros and -inf; rows behind
     row_offsets[B] are not written (they are undefined in an ``out`` that the call allocates)."""
 
@@ -783,8 +790,8 @@ def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Op
     if rows:
         w = _kv_scratch(rows, step.B, heads, cache, 0, dt, ws, "pivot_kv_attention")
         _check(lib().pivot_kv_attention(
-            cache._ref, ctypes.byref(step), q.data_ptr(), qs, heads, dt, d ** -0.5 if scale is None else scale, window,
-            sinks, out.data_ptr(), None if lse is None else lse.data_ptr(), w.data_ptr(), w.numel(),
+            cache._ref, ctypes.byref(step), q.data_ptr(), qs, heads, dt, d ** -0.5 if scale is None else scale,
+            min(window, _FAR), min(sinks, _FAR), out.data_ptr(), None if lse is None else lse.data_ptr(), w.data_ptr(), w.numel(),
             _raw_stream(cache.device.index)), "pivot_kv_attention")
     return out, lse
 

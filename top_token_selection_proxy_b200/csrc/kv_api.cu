@@ -9,6 +9,8 @@ using namespace pivot;
 
 namespace {
 
+constexpr float kLog2e = 1.4426950408889634f;
+
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
 pivot_status check_cache(const pivot_kv_cache* c) {
@@ -34,6 +36,14 @@ pivot_status check_rows(const void* p, int64_t stride, int64_t heads, int d, piv
   const int64_t esz = dt == PIVOT_BF16 ? 2 : 4;
   if (!p || stride < heads * d || !aligned(p, 16) || stride * esz % 16) return PIVOT_ERR_INVALID_ARG;
   return PIVOT_OK;
+}
+
+// Whether the outputs share memory with the queries (which cut items read again after others were written).
+bool out_overlaps(const pivot_kv_cache& c, const pivot_kv_step& s, const void* q, int64_t q_stride, int q_heads,
+                  pivot_dtype dt, const void* out) {
+  const int64_t esz = dt == PIVOT_BF16 ? 2 : 4, row = (int64_t)q_heads * c.d;
+  const char *q0 = static_cast<const char*>(q), *o0 = static_cast<const char*>(out);
+  return o0 < q0 + ((s.rows - 1) * q_stride + row) * esz && q0 < o0 + s.rows * row * esz;
 }
 
 KvCache device_cache(const pivot_kv_cache& c) {
@@ -99,7 +109,7 @@ pivot_status attention_args(const pivot_kv_cache* cache, const pivot_kv_step* st
   if (st != PIVOT_OK) return st;
   if (dt != PIVOT_BF16 && dt != PIVOT_F32) return PIVOT_ERR_INVALID_ARG;
   if (q_heads <= 0 || q_heads % cache->kv_heads || !out || !aligned(out, 16) || !ws || !aligned(ws, 256) ||
-      !std::isfinite(scale))
+      !std::isfinite(scale * kLog2e))
     return PIVOT_ERR_INVALID_ARG;
   st = check_rows(q, q_stride, q_heads, cache->d, dt);
   if (st != PIVOT_OK) return st;
@@ -111,7 +121,7 @@ pivot_status attention_args(const pivot_kv_cache* cache, const pivot_kv_step* st
   a->q_stride = q_stride;
   a->hq = q_heads;
   a->group = q_heads / cache->kv_heads;
-  a->scale2 = scale * 1.4426950408889634f;
+  a->scale2 = scale * kLog2e;
   a->is_bf16 = dt == PIVOT_BF16;
   return PIVOT_OK;
 }
@@ -188,6 +198,7 @@ pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step
   a.window = window;
   a.sinks = sinks;
   if (step->rows == 0) return PIVOT_OK;
+  if (out_overlaps(*cache, *step, q, q_stride, q_heads, dt, out)) return PIVOT_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (many_rows(step->rows, step->B, q_heads, cache->kv_heads, cache->d, dt) &&
@@ -220,6 +231,7 @@ pivot_status pivot_kv_attention_selected(const pivot_kv_cache* cache, const pivo
   a.idx_stride = index_stride;
   a.topk = topk;
   if (step->rows == 0) return PIVOT_OK;
+  if (out_overlaps(*cache, *step, q, q_stride, q_heads, dt, out)) return PIVOT_ERR_INVALID_ARG;
   const cudaError_t e = launch_kv_attn(a, sms(), ws, nullptr, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv selected attention kernel");
 }
