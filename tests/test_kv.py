@@ -1,5 +1,7 @@
 """The paged 8-bit key/value cache on the GPU: kv_append, kv_attention and kv_attention_selected against the 64-bit
 forms of kv_reference.py, alone and as they are used together with the indexer."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -564,6 +566,25 @@ def test_results_do_not_change_from_call_to_call():
     for _ in range(5):
         b = P.kv_attention(q, cache, table, off, ln, lse=True) + P.kv_attention_selected(q, cache, idx, table, off, ln, lse=True)
         assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_fp32_small_weights_keep_their_bits(d):
+    """Half of the dims come from tokens of weight 1024.5 * 2^-26 alone: the heavy tokens' values are 0 there.  The weight
+    stands between two fp16 values of 4 times it, so that what one of them leaves must not be lost."""
+    table, off, ln, pages = make_step([300], [2], 32, 1)
+    cache = make_cache(pages, 1, 32, d, 2)
+    cache.k_exp.zero_(), cache.v_exp.zero_()
+    k, v = cache.k.float().zero_(), cache.v.float().abs()
+    for page in table[0, :4].tolist():  # a heavy token in each 32, so that every warp's reference is one's score
+        k[page, 0, 3, 0] = 11.0
+        v[page, 0, 3, : d // 2], v[page, 0, 3, d // 2:] = 448.0, 0.0
+    cache.k.copy_(k.to(cache.k.dtype)), cache.v.copy_(v.to(cache.v.dtype))
+    q = torch.zeros((2, 3, d), device="cuda")
+    q[..., 0] = math.log(2.0 ** 26 / 1024.5) / 11
+    check_attention(q, cache, table, off, ln, q.dtype, scale=1.0)
+    idx = torch.arange(300, dtype=torch.int32, device="cuda").flip(0).repeat(2, 1).contiguous()
+    check_attention(q, cache, table, off, ln, q.dtype, scale=1.0, indices=idx)
 
 
 def test_arguments_past_64_bits_and_a_workspace_elsewhere():

@@ -31,6 +31,7 @@ constexpr int kWTok = 32;               // tokens a warp takes at a time (two bl
 constexpr int kTile = kWTok * kWarps;   // tokens of a tile
 constexpr int kItemCost = 4;            // what an item costs beside its tiles, in tiles
 constexpr int kWholeTiles = 2;          // items of so few tiles are not cut
+constexpr float kRest = 2048.f;         // fp32: what a weight's fp16 leaves goes into the product times 2^11
 constexpr float kLift = 2.f;            // a weight of the row's reference is 2^2 in fp16
 
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -463,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_
 
       // weights: p for the sum, p * 2^(ve + 2) for the product.  Where a row's do not fit fp16, or it has no reference
       // yet, it takes a new one from the scores in hand, and its sums so far are scaled down.
-      uint32_t pa[2][4], pb[2][4];  // operands of the two blocks; the rest of them (fp32)
+      uint32_t pa[2][4], pb[2][4];  // operands of the two blocks; fp32: 2^11 times the rest of them
       float psum[2];
 #pragma unroll 1
       for (bool fresh = true;; fresh = false) {
@@ -491,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_
             pa[j / 2][2 * (j % 2) + i] = hw;
             if (!BF16) {
               const __half2 hh = *reinterpret_cast<const __half2*>(&hw);
-              pb[j / 2][2 * (j % 2) + i] = pack_f16(w[i][0] - __low2float(hh), w[i][1] - __high2float(hh));
+              pb[j / 2][2 * (j % 2) + i] = pack_f16((w[i][0] - __low2float(hh)) * kRest, (w[i][1] - __high2float(hh)) * kRest);
             }
           }
         }
@@ -589,7 +590,11 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_
                 mma16816(o[4 * k + q4], pa[u], b0[q4], b1[q4]);
               } else {  // fp32: a block's own sum first, then one addition
                 float t4[4] = {0.f, 0.f, 0.f, 0.f};
-                if (!BF16) mma16816(t4, pb[u], b0[q4], b1[q4]);
+                if (!BF16) {
+                  mma16816(t4, pb[u], b0[q4], b1[q4]);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) t4[i] *= 1.f / kRest;
+                }
                 mma16816(t4, pa[u], b0[q4], b1[q4]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
