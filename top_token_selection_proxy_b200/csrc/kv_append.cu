@@ -10,6 +10,12 @@
 // and written).  A block is two warps' work for one head and one of k and v: its (up to 16) token rows stay in
 // registers between the maximum and the rounding, so nothing is read twice; 8 elements a lane, 16-byte loads.
 // Query rows are other CTAs' work: a warp keeps a row's angles and takes its heads in batches of loads.
+//
+// Measured: a prompt of 8192 tokens, 8 key heads and 64 query heads of 128, bf16: 79 us, 4.1 TB/s (62 % of the measured
+// copy bandwidth); 9 prompts of up to 1900 tokens, 24 and 3 heads, together: 27 us (50 %); one token for each of 32
+// sequences: 5 us on the GPU, which is latency.  The next bound is the issue slots (53 % of their peak): the keys'
+// two-float rotation takes some 15 operations an element, where a plain fp32 one would now and then land on the wrong
+// side of an e4m3 tie.
 #include "kv.cuh"
 
 namespace pivot {

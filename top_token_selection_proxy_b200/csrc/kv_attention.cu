@@ -16,8 +16,15 @@
 //
 // Work is cut evenly whatever the lengths are: all tiles of 128 tokens of all (sequence, key head, 16 query rows)
 // stand in one line, each item behind a few places for what it costs beside its tiles, and every CTA takes an equal
-// stretch of it.  A stretch that begins or ends inside an item
-// leaves a partial result, which kv_merge_kernel joins in a fixed order.
+// stretch of it.  A stretch that begins or ends inside an item leaves a partial result, which kv_merge_kernel joins in
+// a fixed order.  (The places: 48 sequences of 1 to 32768 tokens, window 1024, d = 64: 60 us without them, 35 us with.)
+//
+// Measured: 16 sequences of 32000 tokens, 8 key heads, one row of 8 query heads each: d = 128 bf16 251 us (4.17 TB/s,
+// 64 % of the measured copy bandwidth), fp32 337 us; d = 64 129 us (62 %).  1 of 200000: 110 us (57 %).  Not DRAM but
+// the warps' own latency holds it there (few warps fit beside the registers that the sums take; 25 % of the tensor
+// pipe's cycles): conversions to fp16, exponentials and products follow one another within a warp.  Selected rows (1024
+// rows of 64 query heads over 2048 tokens each): 480 us; each of the 4 groups of 16 heads gathers the list for itself,
+// from L2.
 #include <type_traits>
 
 #include "kv.cuh"
@@ -106,7 +113,11 @@ struct Place {
 // ---------------------------------------------------------------- the kernel
 template <int D, bool BF16, bool SEL>
 struct Shape {
-  static constexpr int kCtas = !BF16 || (D == 128 && !SEL) ? 2 : 3;  // an SM holds
+  // CTAs an SM holds, and stages of a warp's ring.  Dense rows of 128 need 255 registers: two CTAs of three stages take
+  // 251 us where three of two take 397 (16 sequences of 32000, bf16).  Selected ones wait for a gather behind two
+  // look-ups, so more warps count for more: three CTAs 480 us, two 542 (1024 rows of 64 heads, lists of 2048; lists of 512
+  // for 64 rows of 8 heads: 24.3 and 22.6).  d = 64: three CTAs 129 us, four 164.
+  static constexpr int kCtas = !BF16 || (D == 128 && !SEL) ? 2 : 3;
   static constexpr int kStages = D == 64 ? 4 : SEL && BF16 ? 2 : 3;
   static constexpr int kKPieces = 4 * (D / 64);         // 16-byte pieces of keys a lane holds of 32 tokens
   static constexpr int kVBytes = D / 8;                 // bytes of a value a lane holds

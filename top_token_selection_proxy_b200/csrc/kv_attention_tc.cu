@@ -5,14 +5,19 @@
 //   S = Q K^T   kind::f8f6f4.  Keys are multiplied as they lie in the cache: TMA brings e4m3 pages into the swizzled
 //               operand layout, nothing is converted.  A bf16 query has 8 bits: two e4m3 parts of 4 bits hold it
 //               (scaled to 2^8; what lies 2^-10 below a row's largest keeps fewer), two products into one sum.
-//   O += P V    kind::f16.  Weights leave the softmax as fp16 and stay in tensor memory, where S was; four warps
-//               turn the values into fp16.
+//   O += P V    kind::f16.  Weights leave the softmax as fp16 and stay in tensor memory; four warps turn the values
+//               into fp16 (an e4m3 product would leave the weights 4 bits).
 // Two tiles are in work at a time, each with its own S, P and softmax warpgroup, into one O: while one is in the
 // softmax, the tensor core multiplies for the other, and a tile's scores are there before its warpgroup has finished
-// the weights of the tile before.  The rows' reference m' passes from tile to tile in shared memory.
+// the weights of the tile before.  A row has one reference u, which lags behind its largest score by what fp16 holds;
+// it passes from tile to tile in shared memory, in the tiles' order, so that results do not depend on timing.
 //
-// What bounds it: the exponentials (16 a clock and SM: 1024 clocks a tile) and the products (1024 clocks) for full
-// items; with half the rows or fewer the cache's bytes.
+// What bounds it: for full items the softmax (a tile's 128 x 128 exponentials are 1024 clocks of an SM, its products
+// 1060, and what else the softmax warps issue comes on top); with half the rows or fewer the cache's bytes.
+// Measured: rows 4096 .. 8191 of a prompt, 32 query and 4 key heads: 540 us, 760 TFLOP/s of the 4 d a visible pair
+// (46 % of the measured bf16 burst).  32 sequences of 16000 to 200000 tokens, 4 rows of 32 heads on 2: 630 us, 3.0 TB/s
+// (46 %), where kv_attention.cu takes 3600.  Four softmax warpgroups, each with half the registers, took 995 and 714 us
+// where two took 662 and 611; loops unrolled (past the instruction cache) twice as long.
 #include <type_traits>
 
 #include "kv.cuh"
@@ -104,7 +109,8 @@ __device__ __forceinline__ int tiles_of(const KvAttnArgs& a, const Seq& s, int r
   return tiles;
 }
 
-// Places in the line of a sequence and one key head: each item's tiles behind kItemCost.  `wide`: the warp's lanes share one sequence's items; else a lane has its own.
+// Places in the line of a sequence and one key head: each item's tiles behind kItemCost.  `wide`: the warp's lanes share
+// one sequence's items; else a lane has its own.
 __device__ __forceinline__ int64_t seq_tiles(const KvAttnArgs& a, const Seq& s, bool wide, int lane) {
   int64_t t = 0;
   for (int rt = wide ? lane : 0; rt < s.row_tiles; rt += wide ? 32 : 1) t += tiles_of(a, s, rt) + kItemCost;
@@ -509,7 +515,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int s = warp / 4, r = tid & 127;
     const uint32_t lanes = (uint32_t)(warp % 4) << 21;  // lane 32 * (warp % 4) in an address' upper half
     const uint32_t sc = tmem + lanes + 128 * s, oc = tmem + lanes + 256, pc = tmem + lanes + 384 + 64 * s;
-    uint32_t n = 0, items = 0, mine = 0, theirs = 0;  // tiles of both halves; items; tiles of this half, of the other before this item
+    // tiles of both halves; items; tiles of this half; of the other before this item
+    uint32_t n = 0, items = 0, mine = 0, theirs = 0;
     bool ok = true;
     // after a failed wait the loop only keeps the barriers' count
     for (; w.live; advance(), ++items) {
