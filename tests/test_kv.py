@@ -747,6 +747,29 @@ def test_long_sequences_rows_together_and_alone(window, sinks):
             assert (one_lse[0] - lse32[r]).abs().max() <= 2.0 ** -18 * lse32[r].abs().max()
 
 
+def test_attention_of_many_rows_weights_that_fall_by_more_than_fp16_holds():
+    """Tokens 128 to 159 give the tile's half a reference of -16; token 170, at -3.5, weighs 2^12.5 by it; token 2, at
+    7.5, lowers all of that by 2^-23.5.  What is left of token 170, 2^-11, must keep its bits."""
+    B, hk = 12, 8  # so many that a CTA takes an item's tiles together
+    table, off, ln, pages = wide_step([300] * B, [100] * B, 4 * hk, hk, 64, 1)
+    cache = make_cache(pages, hk, 64, 128, 2)
+    cache.k_exp.zero_(), cache.v_exp.zero_()
+    k, v = torch.zeros(cache.k.shape, device="cuda"), torch.zeros(cache.v.shape, device="cuda")
+    k[..., 0] = -16.0
+    for s, z, half in ((2, 7.5, 0), (170, -3.5, 1)):
+        for page in table[:, s // 64].tolist():
+            k[page, :, s % 64, 0] = z
+            v[page, :, s % 64, 64 * half:64 * half + 64] = 1.0
+    cache.k.copy_(k.to(cache.k.dtype)), cache.v.copy_(v.to(cache.v.dtype))
+    q = torch.zeros((B * 100, 4 * hk, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    out, _ = P.kv_attention(q, cache, table, off, ln, scale=math.log(2.0))
+    w = 2.0 ** -11 / (1 + 2.0 ** -11 + 298 * 2.0 ** -23.5)
+    # the output's rounding, the weight's two, and the scores' and exponentials' errors, which are far smaller
+    assert ((out[..., 64:].double() / w - 1).abs() <= 2.0 ** -8 + 2 * 2.0 ** -11 + 2.0 ** -16).all()
+    assert ((out[..., :64].double() - 1).abs() <= 2.0 ** -8).all()
+
+
 @pytest.mark.parametrize("B,length,new,hq,hk,window", [
     (4, 8000, 4, 64, 8, 0),      # items of 32 rows: warps without rows beside one that has them
     (2, 8000, 4, 40, 8, 0),      # of 20

@@ -599,9 +599,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int kk = k + tile0, base = (kk < ahead ? kk : kk + gap) * kTok;
         const uint32_t present = me.present;
         const bool whole = present == 0xFFu && base + kTok - 1 <= whole_upto && (base >= whole_from || base + kTok <= sinks);
-        auto load = [&](int c, auto all, uint32_t (&x)[32]) {  // 32 scores; hidden ones -inf
-          tmem_ld32x32b_x32(sc + 32 * c, x);
-          tmem_wait_ld();
+        auto hide = [&](int c, auto all, uint32_t (&x)[32]) {  // of 32 scores, hidden ones become -inf
           if (!all) {
             auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; };
             const int c0 = base + 32 * c;
@@ -620,8 +618,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // After an item's first tiles that is rare.  (The loops are not unrolled, and masked tiles have code of their
         // own: the code then stays in the instruction cache.  Unrolled it ran at half the speed, and in one copy the
         // compiler masks every tile.)
-        auto scale_weights = [&](int columns, float f) {  // this tile's first ones
-          const __half2 fh = __float2half2_rn(f);
+        // This tile's first weights, times f.  A factor below fp16's normal range is applied as two: a weight of 2^15 times
+        // it is still one that counts.  (Products in fp32 would be 64 instructions more in each of three places: the whole
+        // kernel took 18 % longer, with two factors 4 %.)
+        auto scale_weights = [&](int columns, float f) {
+          const __half2 f1 = __float2half2_rn(fmaxf(f, 0x1p-14f)), f2 = __float2half2_rn(fminf(f * 0x1p14f, 1.f));
           tmem_wait_st();
 #pragma unroll 1
           for (int q = 0; q < columns; q += 16) {
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
 #pragma unroll
             for (int j = 0; j < 16; ++j) {
-              const __half2 h = __hmul2(*reinterpret_cast<const __half2*>(&y[j]), fh);
+              const __half2 h = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&y[j]), f1), f2);
               y[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
             tmem_st32x32b_x16(pc + q, y);
@@ -640,14 +641,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 1
           for (int c = 0; c < 4; ++c) {
             uint32_t x[32], y[16];
-            load(c, all, x);
+            tmem_ld32x32b_x32(sc + 32 * c, x);
+            const float2 ks = *reinterpret_cast<const float2*>(&me.ks[2 * c]), ve = *reinterpret_cast<const float2*>(&me.ve[2 * c]),
+                         iv = *reinterpret_cast<const float2*>(&me.iv[2 * c]);
+            const float cb[2] = {factor(ks.x), factor(ks.y)};
+            tmem_wait_ld();
+            stay(x);
             if (c == 3) {  // S may be overwritten
               tc_fence_before();
               mbar_arrive(&T.sc[s]);
             }
-            const float2 ks = *reinterpret_cast<const float2*>(&me.ks[2 * c]), ve = *reinterpret_cast<const float2*>(&me.ve[2 * c]),
-                         iv = *reinterpret_cast<const float2*>(&me.iv[2 * c]);
-            const float cb[2] = {factor(ks.x), factor(ks.y)};
+            hide(c, all, x);
             float part = 0.f;
 #pragma unroll 1
             for (bool first = true;; first = false) {
