@@ -14,9 +14,9 @@
 //
 // What bounds it: for full items the softmax (a tile's 128 x 128 exponentials are 1024 clocks of an SM, its products
 // 1060, and what else the softmax warps issue comes on top); with half the rows or fewer the cache's bytes.
-// Measured: rows 4096 .. 8191 of a prompt, 32 query and 4 key heads: 540 us, 760 TFLOP/s of the 4 d a visible pair
-// (46 % of the measured bf16 burst).  32 sequences of 16000 to 200000 tokens, 4 rows of 32 heads on 2: 630 us, 3.0 TB/s
-// (46 %), where kv_attention.cu takes 3600.  Four softmax warpgroups, each with half the registers, took 995 and 714 us
+// Measured: rows 4096 .. 8191 of a prompt, 32 query and 4 key heads: 547 us, 753 TFLOP/s of the 4 d a visible pair
+// (46 % of the measured bf16 burst).  32 sequences of 16000 to 200000 tokens, 4 rows of 32 heads on 2: 600 us, 3.2 TB/s
+// (48 %), where kv_attention.cu takes 3600.  Four softmax warpgroups, each with half the registers, took 995 and 714 us
 // where two took 662 and 611; loops unrolled (past the instruction cache) twice as long.
 #include <type_traits>
 
