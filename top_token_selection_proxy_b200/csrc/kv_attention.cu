@@ -826,8 +826,9 @@ cudaError_t launch_line(const KvAttnArgs& a, int ctas, const KvLine& line, cudaS
 
 }  // namespace
 
+// Of the most CTAs an SM holds.
 size_t kv_attn_workspace(int sms, int d) {
-  return 256 + (size_t)4 * sms * (sizeof(KvOpen) + 2 * kv_part_floats(kRowsT, d) * sizeof(float));
+  return 256 + (size_t)3 * sms * (sizeof(KvOpen) + 2 * kv_part_floats(kRowsT, d) * sizeof(float));
 }
 
 cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, int rows, bool many, float lift,
