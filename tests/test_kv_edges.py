@@ -1,0 +1,68 @@
+"""Edges of the key/value cache calls: values that are not finite or leave fp32, arguments at the ends of their types,
+caches and queries that a call must not take, and waits that run out."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+import top_token_selection_proxy_b200 as P
+from test_kv import angles, check_attention, gen, host, make_cache, make_q, make_step, payload, wide_step
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from top_token_selection_proxy_b200 import build
+
+    build.build()
+
+
+gpu = pytest.mark.gpu
+
+
+# ---------------------------------------------------------------- append
+
+
+def append_bit_for_bit(x, cos, sin, interleaved, rot, page=16):
+    """Appends x [tokens, heads, d] as one sequence's keys and values; payload and exponents are the definition's."""
+    n, hk, d = x.shape
+    table, off, lens, pages = make_step([n], [n], page, 1)
+    cache = make_cache(pages, hk, page, d, 2)
+    want, exps = host(cache.k), cache.k_exp.cpu().numpy().astype(np.int64)
+    P.kv_append(cache, x, x, table, off, lens, cos=cos, sin=sin, interleaved=interleaved)
+    c64, s64 = (host(cos), host(sin)) if rot else (None, None)
+    with np.errstate(all="ignore"):
+        R.append(want, exps, table.cpu().numpy(), [0, n], [n], host(x), c64, s64, interleaved)
+    assert np.array_equal(cache.k_exp.cpu().numpy(), exps)
+    got = host(cache.k)
+    same = (got == want) | (np.isnan(got) & np.isnan(want))
+    assert same.all(), f"{(~same).sum()} differ: {got[~same][:4]} for {want[~same][:4]}"
+    return cache
+
+
+@gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rot", [64, 32])
+def test_append_rotated_keys_that_are_not_finite_or_leave_fp32(dtype, interleaved, rot):
+    """Infinities stay infinite through the rotation (payload +-448, no part in the scale), NaN stays NaN, and a finite
+    pair whose rotated value no fp32 holds counts as the finite value that it is (exponent 60, payload +-448)."""
+    x = torch.randn((90, 2, 64), device="cuda", generator=gen(1)).to(dtype)
+    inf, nan = float("inf"), float("nan")
+    x[1, 0, 3], x[2, 1, 5], x[3, 0, 7] = inf, -inf, nan
+    x[20, :, 0:40] = inf                # both of a pair: inf - inf is NaN in one of them
+    x[37] = 3e38                        # rotated: 0.2 and 1.4 times that
+    x[50, 0] = -3e38
+    x[50, 1, 9] = nan                   # beside finite values only
+    x[66, 0, 11], x[67, 0, 12] = 3e38, inf
+    cos, sin = torch.full((128, rot // 2), 0.8, device="cuda"), torch.full((128, rot // 2), 0.6, device="cuda")
+    cos[60:, 5], sin[60:, 5] = 0.0, 1.0
+    sin[70:] = -0.6
+    append_bit_for_bit(x, cos, sin, interleaved, rot)
+    # angles with a gain, as long-context tables have them: both products leave fp32, their difference need not
+    x = torch.randn((20, 1, 64), device="cuda", generator=gen(3)).to(dtype)
+    x[4], x[18, :, 2] = 3e38, -3e38
+    append_bit_for_bit(x, cos * 2, sin * 2.5, interleaved, rot)
+    append_bit_for_bit(x, torch.full_like(cos, 1.5), torch.full_like(sin, 1.5), interleaved, rot)

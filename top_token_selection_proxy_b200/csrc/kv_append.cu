@@ -23,6 +23,7 @@ namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
 constexpr int kE = 8;  // elements a lane holds of a row
+constexpr float kMax = 3.402823466e38f;  // the largest finite fp32
 
 // 8 elements as they lie in memory, and as fp32.
 template <bool BF16>
@@ -151,7 +152,18 @@ struct TurnedOdd {
     const float rest = __fsub_rn(low, __fsub_rn(hi, sum));
     const int bits = __float_as_int(hi);
     if ((rest > 0.f || rest < 0.f) && !(bits & 1)) return __int_as_float((rest > 0.f) == (hi > 0.f) ? bits + 1 : bits - 1);
-    return hi;  // exact, odd already, or not finite
+    return hi;  // exact or odd already; NaN wherever a product or the sum is not finite
+  }
+};
+
+// The same where the value's terms may leave fp32.  fp64 holds every product of two fp32 values: NaN and infinities are
+// the formula's, and a finite value that no fp32 holds becomes the largest one, which is past every scale.
+struct TurnedFar {
+  __device__ float operator()(float a, float c, float b, float s) const {
+    const float near = TurnedOdd{}(a, c, b, s);
+    if (fabsf(near) <= kMax) return near;
+    const double v = fma((double)a, (double)c, (double)b * (double)s);
+    return isfinite(v) ? (float)fmin(fmax(v, -(double)kMax), (double)kMax) : (float)v;
   }
 };
 
@@ -194,7 +206,13 @@ __device__ __forceinline__ uint32_t pack4(float a, float b, float c, float d) {
 
 __device__ __forceinline__ float finite_abs(float y) {
   const float a = fabsf(y);
-  return a <= 3.402823466e38f ? a : 0.f;  // NaN and infinities do not set the scale
+  return a <= kMax ? a : 0.f;  // NaN and infinities do not set the scale
+}
+
+__device__ __forceinline__ float max_or_nan(float a, float b) {  // NaN where either is
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 
 // What the two warps of a block tell each other: the largest value of each half.  One set for each block in turn
@@ -228,16 +246,21 @@ __device__ __forceinline__ void append_block(const KvAppendArgs& a, Pair& pair, 
     if (rot) rotate<BF16>(raw[i], y[i], t, angles_at(t, t.on && p >= p0 && p < p1, a.cos, a.sin, p, a.rot / 2), TurnedOdd{});
     else widen<BF16>(raw[i], y[i]);
 #pragma unroll
-    for (int j = 0; j < kE; ++j) amax = fmaxf(amax, fabsf(y[i][j]));  // passes over NaN
+    for (int j = 0; j < kE; ++j) amax = max_or_nan(amax, fabsf(y[i][j]));
   }
 #pragma unroll
-  for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
-  if (!(amax <= 3.402823466e38f)) {  // infinities do not set the scale
+  for (int o = 16; o; o >>= 1) amax = max_or_nan(amax, __shfl_xor_sync(~0u, amax, o));
+  if (!(amax <= kMax)) {  // rare: the rows once more, with care for what is not finite, which does not set the scale
     amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
+    for (int i = 0; i < kPasses; ++i) {
+      const uint32_t p = base + i * kRows + slot;
+      const bool live = p >= p0 && p < p1;
+      const Raw<BF16> again = load8<BF16>(src, (row0 + (p - p0)) * stride + head * D + sub * kE, live);
+      if (rot) rotate<BF16>(again, y[i], t, angles_at(t, t.on && live, a.cos, a.sin, p, a.rot / 2), TurnedFar{});
 #pragma unroll
       for (int j = 0; j < kE; ++j) amax = fmaxf(amax, finite_abs(y[i][j]));
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(~0u, amax, o));
   }
