@@ -418,9 +418,10 @@ PIVOT_API int pivot_path(int op, int64_t L, int H, int d, int k, int c, int g, p
 
 /* Bound (nanoseconds of wall-clock time) on every device-side wait; default
  * 2e9.  Test hooks (pivot_set_debug_flags, process-wide, 0 = normal):
- *   bit 0 (1): the scan kernel waits on a barrier that nothing signals, so
- *              the bound runs out and the timeout path is exercised without
- *              hanging the GPU;
+ *   bit 0 (1): the scan kernel, and pivot_kv_attention's kernel for many
+ *              rows, wait on a barrier that nothing signals, so the bound
+ *              runs out and the timeout path is exercised without hanging
+ *              the GPU;
  *   bit 1 (2): the scan visits key tiles in natural order (no sampled
  *              threshold estimate);
  *   bit 2 (4): the sampled estimate is taken at the sample's best entry, so

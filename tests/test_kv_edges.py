@@ -66,3 +66,28 @@ def test_append_rotated_keys_that_are_not_finite_or_leave_fp32(dtype, interleave
     x[4], x[18, :, 2] = 3e38, -3e38
     append_bit_for_bit(x, cos * 2, sin * 2.5, interleaved, rot)
     append_bit_for_bit(x, torch.full_like(cos, 1.5), torch.full_like(sin, 1.5), interleaved, rot)
+
+
+# ---------------------------------------------------------------- attention of many rows: waits that run out
+
+
+@gpu
+@pytest.mark.parametrize("lens", [[1900, 300, 40], [5000]])
+def test_attention_of_many_rows_whose_wait_runs_out_ends_and_says_so(lens):
+    table, off, ln, pages = wide_step(lens, [30] * len(lens), 8, 2, 64, 1)
+    cache = make_cache(pages, 2, 64, 128, 2)
+    q = make_q(30 * len(lens), 16, 128, "bf16", 3)
+    ws = P.Workspace("cuda")
+    want = P.kv_attention(q, cache, table, off, ln, lse=True, ws=ws)
+    assert P.last_device_status(ws) == 0
+    try:
+        P.set_device_timeout_ns(50_000_000)
+        P.set_debug_flags(1)
+        P.kv_attention(q, cache, table, off, ln, lse=True, ws=ws)
+        assert P.last_device_status(ws) == 5  # PIVOT_ERR_DEVICE_TIMEOUT
+    finally:
+        P.set_debug_flags(0)
+        P.set_device_timeout_ns(2_000_000_000)
+    got = P.kv_attention(q, cache, table, off, ln, lse=True, ws=ws)
+    assert P.last_device_status(ws) == 0
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

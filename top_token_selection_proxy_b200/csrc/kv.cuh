@@ -102,7 +102,7 @@ cudaError_t launch_kv_merge(const KvAttnArgs& a, const KvLine& line, int ctas, i
                             cudaStream_t s);
 size_t kv_attn_tc_workspace(int sms, int d);
 cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms, void* ws,
-                              uint64_t timeout_ns, cudaStream_t s);
+                              uint64_t timeout_ns, bool stall, cudaStream_t s);
 
 // The sequence b with off[b] <= r < off[b+1], or -1.
 __device__ __forceinline__ int kv_sequence_of(const KvStep& st, int64_t r) {

@@ -207,7 +207,7 @@ pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step
     CUtensorMap kmap, vmap;
     if (!payload_map(&kmap, cache->k, slots) || !payload_map(&vmap, cache->v, slots))
       return record_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
-    e = launch_kv_attn_tc(a, kmap, vmap, sms(), ws, device_timeout_ns(), s);
+    e = launch_kv_attn_tc(a, kmap, vmap, sms(), ws, device_timeout_ns(), debug_flags() & 1, s);
   } else {
     e = launch_kv_attn(a, sms(), ws, nullptr, s);
   }

@@ -46,6 +46,7 @@ struct TcArgs {
   int* gate;            // set where a masked place holds a NaN value
   int64_t slots;        // rows of the cache's tensor maps
   uint64_t timeout_ns;
+  bool stall;           // test hook: the product waits for weights of a thread that there is not
 };
 
 // ---------------------------------------------------------------- items: 128 query rows of a sequence and key head
@@ -298,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < kVS; ++i) mbar_init(&T.vf[i], 1), mbar_init(&T.ve[i], kConv);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&T.hf[i], kConv), mbar_init(&T.he[i], 1);
-      mbar_init(&T.sf[i], 1), mbar_init(&T.sc[i], kSoft / 2), mbar_init(&T.pf[i], kSoft / 2);
+      mbar_init(&T.sf[i], 1), mbar_init(&T.sc[i], kSoft / 2), mbar_init(&T.pf[i], kSoft / 2 + args.stall);
       mbar_init(&T.rf[i], kSoft / 2), mbar_init(&T.od[i], 1);
     }
     for (int i = 0; i < kMeta; ++i) mbar_init(&T.mf[i], 1);
@@ -509,6 +510,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         mbar_arrive(&T.hf[hb]);
         mbar_arrive(&T.ve[vs]);
       }
+      // One lane's wait may run out where another's did not: they leave together, or they would wait for one another at
+      // different barriers.
+      ok = __all_sync(~0u, ok);
     }
   } else {
     // ------------------------------------------------------------ softmax: a thread for a row, a warpgroup for a half
@@ -817,7 +821,7 @@ size_t kv_attn_tc_workspace(int sms, int d) {
 }
 
 cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap, int sms, void* ws,
-                              uint64_t timeout_ns, cudaStream_t s) {
+                              uint64_t timeout_ns, bool stall, cudaStream_t s) {
   cudaError_t e = cudaMemsetAsync(ws, 0, 256, s);
   if (e != cudaSuccess) return e;
   char* p = static_cast<char*>(ws);
@@ -829,6 +833,7 @@ cudaError_t launch_kv_attn_tc(const KvAttnArgs& a, const CUtensorMap& kmap, cons
   t.line.part = reinterpret_cast<float*>(p + 256 + (size_t)sms * sizeof(KvOpen));
   t.slots = (int64_t)a.c.pages * a.c.hk * a.c.ps;
   t.timeout_ns = timeout_ns;
+  t.stall = stall;
   e = kv_allow_smem<kv_attn_tc_kernel>(kSmem);
   if (e != cudaSuccess) return e;
   kv_attn_tc_kernel<<<sms, kThreads, kSmem, s>>>(kmap, vmap, t);
