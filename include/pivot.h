@@ -382,8 +382,9 @@ PIVOT_API pivot_status pivot_kv_append(const pivot_kv_cache *cache, const pivot_
  * largest, with an error of at most 2^-25 (fp32: 2^-38) of that.
  * The same call gives the same bits every time.  out must not overlap q.
  * ws: pivot_kv_workspace_size bytes on the current device (256-byte aligned; 0: the call would be refused), with
- * topk 0 for pivot_kv_attention.  pivot_last_device_status reads it.  None of these calls records the events of
- * pivot_set_profile_events. */
+ * topk 0 for pivot_kv_attention.  pivot_last_device_status reads it: a wait that ran out is reported there, and the
+ * rows were then computed again by a kernel that waits for nothing, so that the outputs hold all the same.  None of
+ * these calls records the events of pivot_set_profile_events. */
 PIVOT_API size_t pivot_kv_workspace_size(int64_t rows, int B, int q_heads, int kv_heads, int d, int topk,
                                          pivot_dtype dt);
 PIVOT_API pivot_status pivot_kv_attention(const pivot_kv_cache *cache, const pivot_kv_step *step, const void *q,

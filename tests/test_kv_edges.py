@@ -85,6 +85,8 @@ def test_attention_of_many_rows_whose_wait_runs_out_ends_and_says_so(lens):
         P.set_debug_flags(1)
         P.kv_attention(q, cache, table, off, ln, lse=True, ws=ws)
         assert P.last_device_status(ws) == 5  # PIVOT_ERR_DEVICE_TIMEOUT
+        # its rows are right all the same, also for a caller who keeps no workspace to ask
+        check_attention(q, cache, table, off, ln, q.dtype)
     finally:
         P.set_debug_flags(0)
         P.set_device_timeout_ns(2_000_000_000)

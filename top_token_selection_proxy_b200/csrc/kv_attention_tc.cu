@@ -43,7 +43,8 @@ struct Meta {  // of a tile's 8 blocks
 struct TcArgs {
   KvAttnArgs a;
   KvLine line;
-  int* gate;            // set where a masked place holds a NaN value
+  int* gate;            // set where kv_attn_kernel must compute the call again: a masked place holds a NaN value, or a
+                        // wait ran out here
   int64_t slots;        // rows of the cache's tensor maps
   uint64_t timeout_ns;
   bool stall;           // test hook: the product waits for weights of a thread that there is not
@@ -290,7 +291,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   Tail& T = *reinterpret_cast<Tail*>(smem + kOffTail);
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled operands need it; there is no room to align
-    if (threadIdx.x == 0) atomicOr(args.line.status, DEV_ERR_BOUNDS);
+    if (threadIdx.x == 0) atomicOr(args.line.status, DEV_ERR_BOUNDS), *args.gate = 1;
     return;
   }
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -807,6 +808,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   __syncthreads();
   if (T.abort_flag) {  // let copies and products in flight end before tensor memory goes
+    if (tid == 0) *args.gate = 1;  // what this CTA leaves undone is computed again, without waits
     const uint64_t t0 = globaltimer_ns();
     while (globaltimer_ns() - t0 < 200000ull) {
     }
