@@ -93,3 +93,36 @@ def test_attention_of_many_rows_whose_wait_runs_out_ends_and_says_so(lens):
     got = P.kv_attention(q, cache, table, off, ln, lse=True, ws=ws)
     assert P.last_device_status(ws) == 0
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ---------------------------------------------------------------- arguments
+
+
+def c_attention(q, cache, table, off, lens, window, sinks):
+    """pivot_kv_attention itself, with arguments that the binding would have made smaller."""
+    out = torch.full(q.shape, 77.0, dtype=q.dtype, device="cuda")
+    step, _keep = P._kv_step(cache, table, off, lens, q.shape[0])
+    dt = P._KV_TYPES[q.dtype]
+    size = P.lib().pivot_kv_workspace_size(q.shape[0], step.B, q.shape[1], cache.kv_heads, cache.d, 0, dt)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    st = P.lib().pivot_kv_attention(cache._ref, ctypes.byref(step), q.data_ptr(), q.stride(0), q.shape[1], dt,
+                                    cache.d ** -0.5, window, sinks, out.data_ptr(), None, ws.data_ptr(), size,
+                                    torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    return out
+
+
+@gpu
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_largest_window_is_no_window(dtype):
+    """Also for sequences of more rows than tokens, whose first rows stand at positions below 0."""
+    table, off, ln, pages = wide_step([300, 5], [305, 20], 4, 1, 32, 1)  # bf16: the kernel for many rows
+    cache = make_cache(pages, 1, 32, 128, 2)
+    q = make_q(325, 4, 128, dtype, 3)
+    want, _ = P.kv_attention(q, cache, table, off, ln)
+    for window in (2 ** 63 - 1, 2 ** 63 - 4, 2 ** 62 + 1):
+        for sinks in (0, 2 ** 63 - 1):
+            assert torch.equal(c_attention(q, cache, table, off, ln, window, sinks), want)
+    # a window with more first tokens than there are
+    assert torch.equal(c_attention(q, cache, table, off, ln, 7, 2 ** 63 - 1), want)

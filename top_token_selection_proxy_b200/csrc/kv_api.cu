@@ -10,6 +10,7 @@ using namespace pivot;
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int64_t kFar = 1ll << 62;  // more tokens than there can be; positions, which may lie below 0, less it fit 64 bits
 
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 
@@ -195,14 +196,14 @@ pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step
   if (ws_bytes < pivot_kv_workspace_size(step->rows, step->B, q_heads, cache->kv_heads, cache->d, 0, dt))
     return PIVOT_ERR_WORKSPACE_TOO_SMALL;
   a.lse = lse_opt;
-  a.window = window;
-  a.sinks = sinks;
+  a.window = std::min(window, kFar);
+  a.sinks = std::min(sinks, kFar);
   if (step->rows == 0) return PIVOT_OK;
   if (out_overlaps(*cache, *step, q, q_stride, q_heads, dt, out)) return PIVOT_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (many_rows(step->rows, step->B, q_heads, cache->kv_heads, cache->d, dt) &&
-      much_work(*cache, *step, q_heads, window, sinks)) {
+      much_work(*cache, *step, q_heads, a.window, a.sinks)) {
     const int64_t slots = (int64_t)cache->num_pages * cache->kv_heads * cache->page_size;
     CUtensorMap kmap, vmap;
     if (!payload_map(&kmap, cache->k, slots) || !payload_map(&vmap, cache->v, slots))
