@@ -126,3 +126,13 @@ def test_the_largest_window_is_no_window(dtype):
             assert torch.equal(c_attention(q, cache, table, off, ln, window, sinks), want)
     # a window with more first tokens than there are
     assert torch.equal(c_attention(q, cache, table, off, ln, 7, 2 ** 63 - 1), want)
+
+
+def test_a_cache_keeps_the_tensors_that_its_calls_write():
+    """The calls go by pointers taken once: an attribute that pointed elsewhere would not be what they write."""
+    cache = P.KVCache.__new__(P.KVCache)
+    for name in ("k", "v", "k_exp", "v_exp", "device", "num_pages", "kv_heads", "page_size", "d", "_c", "_ref", "x"):
+        with pytest.raises(AttributeError):
+            setattr(cache, name, torch.zeros(1))
+        with pytest.raises(AttributeError):
+            delattr(cache, name)

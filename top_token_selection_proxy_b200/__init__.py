@@ -596,7 +596,11 @@ class KVCache:
     k, v: float8_e4m3fn [num_pages, kv_heads, page_size, d] (d = 64 or 128); k_exp, v_exp: int8
     [num_pages, kv_heads, page_size / KV_BLOCK].  A key is payload * 2**k_exp of its block of KV_BLOCK
     tokens and head.  The tensors are the caller's, contiguous and on one device; the cache keeps
-    references to them and the calls below write them in place.  ``KVCache.empty`` allocates them."""
+    references to them and the calls below write them in place, where they lay when the cache was made: its
+    attributes are fixed, and the tensors' storage must stay.  ``KVCache.empty`` allocates them."""
+
+    __slots__ = ("k", "v", "k_exp", "v_exp", "device", "num_pages", "kv_heads", "page_size", "d", "_c", "_ref",
+                 "__weakref__")
 
     def __init__(self, k, v, k_exp, v_exp):
         if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
@@ -611,10 +615,16 @@ class KVCache:
         _need_cuda(k, v, k_exp, v_exp)
         if len({t.device for t in (k, v, k_exp, v_exp)}) != 1:
             raise ValueError("k, v, k_exp and v_exp must be on one device")
-        self.k, self.v, self.k_exp, self.v_exp = k, v, k_exp, v_exp
-        self.device, self.num_pages, self.kv_heads, self.page_size, self.d = k.device, pages, heads, page, d
-        self._c = _CacheC(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, heads, page, d)
-        self._ref = ctypes.byref(self._c)
+        c = _CacheC(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, heads, page, d)
+        for name, value in zip(self.__slots__, (k, v, k_exp, v_exp, k.device, pages, heads, page, d, c,
+                                                ctypes.byref(c))):
+            object.__setattr__(self, name, value)
+
+    def __setattr__(self, name, value):  # the C struct would go on pointing at what was there
+        raise AttributeError(f"a KVCache's {name} cannot be changed; make another KVCache")
+
+    def __delattr__(self, name):
+        self.__setattr__(name, None)
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, d: int, device="cuda") -> "KVCache":
