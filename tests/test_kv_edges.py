@@ -136,3 +136,28 @@ def test_a_cache_keeps_the_tensors_that_its_calls_write():
             setattr(cache, name, torch.zeros(1))
         with pytest.raises(AttributeError):
             delattr(cache, name)
+
+
+@gpu
+def test_rows_that_require_a_gradient_are_refused():
+    table, off, ln, pages = make_step([20], [2], 16, 1)
+    cache = make_cache(pages, 2, 16, 64, 2)
+    q, k, v = make_q(2, 4, 64, "f32", 3), make_q(2, 2, 64, "f32", 4), make_q(2, 2, 64, "f32", 5)
+    idx = torch.zeros((2, 3), dtype=torch.int32, device="cuda")
+    before = payload(cache.k).copy()
+    want, _ = P.kv_attention(q, cache, table, off, ln)
+    grown = q.clone().requires_grad_(True)
+    calls = [lambda x: P.kv_attention(x, cache, table, off, ln)[0],
+             lambda x: P.kv_attention_selected(x, cache, idx, table, off, ln)[0],
+             lambda x: P.kv_append(cache, k, v, table, off, ln, q=x),
+             lambda x: P.kv_append(cache, x[:, :2], v, table, off, ln),
+             lambda x: P.kv_append(cache, k, x[:, 2:], table, off, ln),
+             lambda x: P.kv_attention(q, cache, table, off, ln, out=x)[0],
+             lambda x: P.kv_append(cache, k, v, table, off, ln, q=q, q_out=x)]
+    for call in calls:
+        with pytest.raises(ValueError, match="gradient"):
+            call(grown)
+    assert np.array_equal(payload(cache.k), before)
+    with torch.no_grad():
+        assert torch.equal(calls[0](grown), want)
+    assert torch.equal(calls[0](grown.detach()), want)

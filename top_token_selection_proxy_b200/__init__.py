@@ -650,7 +650,8 @@ def _kv_elsewhere(cache, stream):
 
 
 def _kv_rows(name, t, heads, cache, dtype=None):
-    """Checks a row tensor [rows, heads, d] whose rows may be slices of a wider one; returns its row stride."""
+    """Checks a row tensor [rows, heads, d] whose rows may be slices of a wider one; returns its row stride.  None of
+    these calls has a backward pass, so one whose gradient would be lost is refused."""
     shape = t.shape
     if len(shape) != 3 or shape[2] != cache.d or (heads and shape[1] != heads):
         raise ValueError(f"{name} must be [rows, {heads or 'heads'}, {cache.d}]")
@@ -658,6 +659,8 @@ def _kv_rows(name, t, heads, cache, dtype=None):
         raise TypeError(f"{name} must be bfloat16 or float32, of the same type as the other rows, got {t.dtype}")
     if t.device != cache.device:
         raise ValueError(f"{name} must be on {cache.device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} requires a gradient, which this call does not pass on: detach it, or use no_grad")
     r, h, e = t.stride()
     if e != 1 or (h != cache.d and shape[1] > 1):
         raise ValueError(f"{name}: each row's heads must be contiguous")
@@ -694,7 +697,8 @@ def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None,
     tensors, DeviceOffsets, or host values (copied on every call).  cos, sin [positions, rot / 2] fp32
     (positions >= width * page_size) rotate the first rot dims of k, and of q [rows, heads, d] into q_out (a new tensor unless given; q
     itself is allowed): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no
-    token, or lie behind the table's width, leave cache and q_out as they were."""
+    token, or lie behind the table's width, leave cache and q_out as they were.  There is no backward pass: k, v or q
+    that require a gradient are refused where gradients are on."""
     other = _kv_elsewhere(cache, stream)
     if other is not None:
         with torch.cuda.stream(other):
@@ -766,6 +770,8 @@ def _kv_results(q, cache, out, lse):
         out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     elif out.shape != q.shape or out.dtype is not q.dtype or out.device != q.device or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape, type and device")
+    elif out.requires_grad and torch.is_grad_enabled():
+        raise ValueError("out requires a gradient, which this call does not pass on")
     if lse is True:
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     elif lse is False:
@@ -773,6 +779,8 @@ def _kv_results(q, cache, out, lse):
     elif lse is not None and (lse.shape != q.shape[:2] or lse.dtype is not torch.float32 or
                               lse.device != q.device or not lse.is_contiguous()):
         raise ValueError("lse must be a contiguous fp32 [rows, heads] tensor on q's device")
+    elif lse is not None and lse.requires_grad and torch.is_grad_enabled():
+        raise ValueError("lse requires a gradient, which this call does not pass on")
     return out, lse
 
 
@@ -785,8 +793,8 @@ def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Op
     first ``sinks``.  ``scale`` defaults to d ** -0.5.  ``out`` must not share memory with q.  ``ws``: scratch kept
     between calls, which must then be ordered (last_device_status reads it); else each call has its own.  ``lse``: False, True, or an fp32 [rows, heads] tensor
     that receives ln sum exp(scale q.k).  Rows that see nothing give zeros and -inf; rows behind
-    row_offsets[B] are not written (they are undefined in an ``out`` that the call allocates)."""
-
+    row_offsets[B] are not written (they are undefined in an ``out`` that the call allocates).  There is no backward
+    pass: a q that requires a gradient is refused where gradients are on."""
     other = _kv_elsewhere(cache, stream)
     if other is not None:
         with torch.cuda.stream(other):
