@@ -161,3 +161,43 @@ def test_rows_that_require_a_gradient_are_refused():
     with torch.no_grad():
         assert torch.equal(calls[0](grown), want)
     assert torch.equal(calls[0](grown.detach()), want)
+
+
+# ---------------------------------------------------------------- attention: values' scales at the ends of their range
+
+
+@gpu
+@pytest.mark.parametrize("heavy", [0, 700, 1400])
+@pytest.mark.parametrize("form", ["f32", "bf16", "bf16 d 64", "selected", "cut f32", "many rows", "cut many rows"])
+def test_tokens_of_small_values_count_in_the_sum_of_weights(form, heavy):
+    """16 tokens with values of 2^60 and more at score 0, all others with values of 2^-60 at score -9 (in units of log 2):
+    the others' values do not show beside the heavy ones, but their weights, 2^-9 each, are a sixth of the sum."""
+    many, cut = "many" in form, "cut" in form
+    d = 64 if form.endswith("64") else 128
+    B, hk, group = (1, 1, 4) if cut or not many else (40, 4, 4)
+    n = 1600 if not cut else 12_800  # cut: one sequence's tiles shared by many CTAs
+    new = (20 if cut else 90) if many else 2
+    step = wide_step([n] * B, [new] * B, hk * group, hk, 64, 1) if many else make_step([n] * B, [new] * B, 64, 1)
+    table, off, ln, pages = step
+    cache = make_cache(pages, hk, 64, d, 2)
+    cache.v_exp.fill_(-60), cache.k_exp.zero_()
+    k = torch.zeros(cache.k.shape, device="cuda")
+    k[..., 0] = -9.0
+    at = heavy * n // 1600 // 16 * 16
+    for page in table[:, at // 64].tolist():
+        cache.v_exp[page, :, at % 64 // 16] = 60
+        k[page, :, at % 64:at % 64 + 16, 0] = 0.0
+    cache.k.copy_(k.to(cache.k.dtype))
+    q = torch.zeros((B * new, hk * group, d), dtype=torch.float32 if "f32" in form else torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    idx = None
+    if form == "selected":
+        idx = torch.arange(n, dtype=torch.int32, device="cuda").repeat(new, 1).contiguous()
+    check_attention(q[:new] if B > 1 else q, cache, table[:1] if B > 1 else table, off[:2] if B > 1 else off,
+                    ln[:1] if B > 1 else ln, q.dtype, scale=math.log(2.0), indices=idx)
+    if B > 1:  # the batch, whose items are not cut: as the sequence alone
+        one = P.kv_attention(q[:new], cache, table[:1], off[:2], ln[:1], scale=math.log(2.0), lse=True)
+        for b in range(B):
+            assert torch.equal(cache.v_exp[table[b, :n // 64].long()], cache.v_exp[table[0, :n // 64].long()])
+        got = P.kv_attention(q, cache, table, off, ln, scale=math.log(2.0), lse=True)
+        assert ((got[1].view(B, new, -1) - one[1]).abs() <= 2.0 ** -12).all()  # 1600 additions in fp32

@@ -122,6 +122,11 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// x * 2^e, e <= 0, where 2^e alone may lie below fp32's normal range: sums over tokens whose values' scales lie far apart.
+__device__ __forceinline__ float kv_down(float x, float e) {
+  return x * ex2(fmaxf(e, -126.f)) * ex2(fminf(e + 126.f, 0.f));
+}
+
 __device__ __forceinline__ uint32_t cvt_e4m3x2(uint32_t two) {  // two e4m3 bytes to two fp16
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));

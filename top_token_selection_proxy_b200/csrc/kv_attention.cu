@@ -525,9 +525,10 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_
                                 __uint_as_float(te[j][k] & 0xFFFF0000u)));
           t = quad_max(t);  // the four lanes of a row decide together
           const bool raise = quad_max(over[i] ? 1.f : 0.f) > 0.f && t > ref[i];
-          f[i] = raise && ref[i] != -INFINITY ? ex2(ref[i] - t) : 1.f;
+          const float down = raise && ref[i] != -INFINITY ? ref[i] - t : 0.f;
+          f[i] = ex2(down);
           if (raise) ref[i] = t;
-          l[i] *= f[i];
+          l[i] = kv_down(l[i], down);
           raised |= raise;
         }
         if (!__any_sync(~0u, raised)) break;
@@ -690,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, Shape<D, BF16, SEL>::kCtas) kv_attn_
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float rw = stats[w * 64 + r * 4], lw = stats[w * 64 + r * 4 + 1];
-        lt += rw == -INFINITY ? lw : lw * ex2(rw - top);  // -inf: zero, or NaN of a score
+        lt += rw == -INFINITY ? lw : kv_down(lw, rw - top);  // -inf: zero, or NaN of a score
       }
       if (all) {
         const int64_t rr = row0 + (rr0 + r) / a.group;
@@ -760,7 +761,8 @@ __global__ void __launch_bounds__(32 * kMergeWarps)
     const float4 v = mine ? *reinterpret_cast<const float4*>(p + r * D + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     const float f = s.x == -INFINITY ? (s.y == 0.f ? 0.f : 1.f) : ex2(s.x - u);  // no reference: nothing, or NaN of a score
     l = fmaf(s.y, f, l);
-    if (f != 0.f) acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
+    if (f == 0.f) l += kv_down(s.y, s.x - u);  // l may count where 2^(s.x - u) alone lies below fp32's normal range
+    else acc.x = fmaf(v.x, f, acc.x), acc.y = fmaf(v.y, f, acc.y), acc.z = fmaf(v.z, f, acc.z), acc.w = fmaf(v.w, f, acc.w);
   }
   if (per_row > 1) {
     if (lane * 4 < D) *reinterpret_cast<float4*>(&sums[warp][lane * 4]) = acc;

@@ -33,6 +33,9 @@ constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWQk = kWTma + 1
 constexpr int kThreads = 32 * (kWPv + 1);
 constexpr int kItemCost = 8;   // what an item costs beside its tiles, in tiles
 constexpr float kLift = 2.f;  // a weight of the row's reference is 2^2 in fp16
+// Values' exponents up to here are this kernel's.  It sums weights 2^(z + ve - u + 2) in fp32, 2^-ve times them for l: with
+// exponents 76 apart at most (they begin at -60), a token of 2^-52 of the row's largest p still counts.
+constexpr int kTopExp = 16;
 
 struct Meta {  // of a tile's 8 blocks
   float ks[8], ve[8], iv[8];  // 2^ke, ve, 2^-ve
@@ -43,8 +46,8 @@ struct Meta {  // of a tile's 8 blocks
 struct TcArgs {
   KvAttnArgs a;
   KvLine line;
-  int* gate;            // set where kv_attn_kernel must compute the call again: a masked place holds a NaN value, or a
-                        // wait ran out here
+  int* gate;            // set where kv_attn_kernel must compute the call again: a masked place holds a NaN value, a value's
+                        // exponent is above kTopExp, or a wait ran out here
   int64_t slots;        // rows of the cache's tensor maps
   uint64_t timeout_ns;
   bool stall;           // test hook: the product waits for weights of a thread that there is not
@@ -398,6 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           m.ks[i] = kv_scale(now.ke);
           m.ve[i] = (float)now.ve;
           m.iv[i] = kv_exp2i(min(-(int)now.ve, 127));
+          if (now.ve > kTopExp && now.slot >= 0) *args.gate = 1;
           if (i == 0) m.present = there >> (8 * (k % 4)) & 0xFFu;
         }
         __syncwarp();
