@@ -201,3 +201,49 @@ def test_tokens_of_small_values_count_in_the_sum_of_weights(form, heavy):
             assert torch.equal(cache.v_exp[table[b, :n // 64].long()], cache.v_exp[table[0, :n // 64].long()])
         got = P.kv_attention(q, cache, table, off, ln, scale=math.log(2.0), lse=True)
         assert ((got[1].view(B, new, -1) - one[1]).abs() <= 2.0 ** -12).all()  # 1600 additions in fp32
+
+
+@gpu
+def test_attention_of_many_rows_rescaled_weights_are_not_biased():
+    """Tokens 0 .. 95 set a tile's reference; token 127 stands 13 + 1 - 0.98 * 2^-11 / ln 2 above it, so that what was
+    weighed before is scaled by a factor just below the middle between two fp16 values.  Half of the dims hold the first
+    tokens' values alone: on average over many independent values their error is the factor's."""
+    B, hk = 4, 8
+    table, off, ln, pages = wide_step([228] * B, [100] * B, 4 * hk, hk, 64, 1)
+    cache = make_cache(pages, hk, 64, 128, 2)
+    cache.k_exp.zero_()
+    cache.v_exp.fill_(-8)
+    k = torch.zeros(cache.k.shape, device="cuda")
+    v = cache.v.float().abs()
+    rise = 14 - 0.98 * 2.0 ** -11 / math.log(2.0)
+    spread = torch.randint(-14, 1, cache.k.shape[:3], device="cuda", generator=gen(9)).float() / 8  # 0 .. -1.75 rises / 16
+    k[..., 0] = spread
+    v[..., 64:] = v[..., 64:] + 1.0
+    tab = table.cpu().numpy()
+    for b in range(B):
+        page = lambda s: int(tab[b, s // 64])
+        for c in (0, 32, 64):
+            k[page(c), :, c % 64, 0] = 0.0     # the largest of the first tokens: the reference
+        for s in range(96, 228):
+            k[page(s), :, s % 64, 0] = -448.0
+            v[page(s), :, s % 64, 64:] = 0.0
+        k[page(127), :, 63, 0] = 16.0
+    cache.k.copy_(k.to(cache.k.dtype)), cache.v.copy_(v.to(cache.v.dtype))
+    q = torch.zeros((B * 100, 4 * hk, 128), dtype=torch.bfloat16, device="cuda")
+    q[..., 0] = 1.0
+    scale = rise / 16 * math.log(2.0)
+    out, _ = P.kv_attention(q, cache, table, off, ln, scale=scale)
+    errors = []
+    for b in range(B):
+        for h in range(hk):
+            pages_b = table[b, :4].long()
+            kk = (cache.k[pages_b, h].double()).reshape(256, 128)[:128, 0]
+            vv = (cache.v[pages_b, h].double() * 2.0 ** -8).reshape(256, 128)[:128]
+            p = torch.exp(kk * scale)
+            want = (p @ vv / p.sum())[64:]
+            errors.append(out[b * 100, 4 * h, 64:].double() / want - 1)
+    errors = torch.cat(errors)
+    # 2048 roundings to bf16 (2^-9 at most each, evenly spread: 2^-9 / sqrt(3 * 2048) for the mean, four times that here),
+    # and the weights' own, 96 to a sum and 32 independent sums (2^-12 / sqrt(3 * 96 * 32) and less)
+    assert abs(float(errors.mean())) <= 4 * 2.0 ** -9 / math.sqrt(3 * 2048) + 2.0 ** -18
+    assert float(errors.abs().max()) <= 2.0 ** -8 + 2.0 ** -10

@@ -32,7 +32,7 @@ constexpr int kSoft = 256, kConv = 128;      // threads: two softmax warpgroups,
 constexpr int kWConv = kSoft / 32, kWTma = kWConv + kConv / 32, kWQk = kWTma + 1, kWPv = kWQk + 1;
 constexpr int kThreads = 32 * (kWPv + 1);
 constexpr int kItemCost = 8;   // what an item costs beside its tiles, in tiles
-constexpr float kLift = 2.f;  // a weight of the row's reference is 2^2 in fp16
+constexpr float kLift = 2.f;  // a weight of the row's reference is 2^2 in fp16, the largest thus 2^2 to 2^3
 // Values' exponents up to here are this kernel's.  It sums weights 2^(z + ve - u + 2) in fp32, 2^-ve times them for l: with
 // exponents 76 apart at most (they begin at -60), a token of 2^-52 of the row's largest p still counts.
 constexpr int kTopExp = 16;
@@ -627,8 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // After an item's first tiles that is rare.  (The loops are not unrolled, and masked tiles have code of their
         // own: the code then stays in the instruction cache.  Unrolled it ran at half the speed, and in one copy the
         // compiler masks every tile.)
-        // This tile's first weights, times f.  A factor below fp16's normal range is applied as two: a weight of 2^15 times
-        // it is still one that counts.  (Products in fp32 would be 64 instructions more in each of three places: the whole
+        // This tile's first weights, times f: a power of two, so that no weight is rounded twice (a factor of 11 bits put all
+        // of a tile's weights off by up to 2^-12 together).  One below fp16's normal range is applied as two: a weight of
+        // 2^15 times it is still one that counts.  (Products in fp32 would be 64 instructions more in each of three places: the whole
         // kernel took 18 % longer, with two factors 4 %.)
         auto scale_weights = [&](int columns, float f) {
           const __half2 f1 = __float2half2_rn(fmaxf(f, 0x1p-14f)), f2 = __float2half2_rn(fminf(f * 0x1p14f, 1.f));
@@ -695,7 +696,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 t0 = fmaxf(t0, __uint_as_float(x[j]));
                 t1 = fmaxf(t1, __uint_as_float(x[16 + j]));
               }
-              const float t = fmaxf(t0 * cb[0] + ve.x, t1 * cb[1] + ve.y);
+              const float t = floorf(fmaxf(t0 * cb[0] + ve.x, t1 * cb[1] + ve.y));  // whole: factors are powers of two
               const bool raise = over && t > u;
               if (!__any_sync(~0u, raise)) break;
               const float f = raise && u != -INFINITY ? ex2(u - t) : 1.f;
