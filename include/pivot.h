@@ -380,7 +380,7 @@ PIVOT_API pivot_status pivot_kv_append(const pivot_kv_cache *cache, const pivot_
  * Scores, softmax statistics and output sums are fp32.  bf16: the weights p enter the output product with 8 bits
  * or more, fp32 with 21 or more; where p 2^e (e the value's exponent) lies under 2^-19 (fp32: 2^-17) of the row's
  * largest, with an error of at most 2^-25 (fp32: 2^-38) of that.
- * The same call gives the same bits every time.  out must not overlap q.
+ * The same call gives the same bits every time.  out, lse_opt and q must not overlap.
  * ws: pivot_kv_workspace_size bytes on the current device (256-byte aligned; 0: the call would be refused), with
  * topk 0 for pivot_kv_attention.  pivot_last_device_status reads it: a wait that ran out is reported there, and the
  * rows were then computed again by a kernel that waits for nothing, so that the outputs hold all the same.  None of

@@ -247,3 +247,16 @@ def test_attention_of_many_rows_rescaled_weights_are_not_biased():
     # and the weights' own, 96 to a sum and 32 independent sums (2^-12 / sqrt(3 * 96 * 32) and less)
     assert abs(float(errors.mean())) <= 4 * 2.0 ** -9 / math.sqrt(3 * 2048) + 2.0 ** -18
     assert float(errors.abs().max()) <= 2.0 ** -8 + 2.0 ** -10
+
+
+@pytest.mark.parametrize("call", ["attend", "select"])
+def test_attention_refuses_a_log_sum_over_the_queries_or_the_outputs(call):
+    import test_kv_abi as A
+
+    run, lib = getattr(A, call), P.lib()
+    rows = 3 * 1024 * 2  # bytes of q, and of out
+    far = A.PTR + 2 * rows
+    for lse in (A.PTR, A.PTR + rows - 4, A.PTR + rows, A.PTR + 2 * rows - 4):  # q, then out
+        assert run(lib, A.cache(), A.step(), q=A.PTR, out=A.PTR + rows, lse=lse) == 1, lse - A.PTR
+    for lse in (far - 3 * 8 * 4 + 4, far - 4, far + rows - 4):
+        assert run(lib, A.cache(), A.step(), q=A.PTR, out=far, lse=lse) == 1, lse - far

@@ -39,12 +39,19 @@ pivot_status check_rows(const void* p, int64_t stride, int64_t heads, int d, piv
   return PIVOT_OK;
 }
 
-// Whether the outputs share memory with the queries (which cut items read again after others were written).
+// Whether the outputs share memory with the queries (which cut items read again after others were written) or with one
+// another.
 bool out_overlaps(const pivot_kv_cache& c, const pivot_kv_step& s, const void* q, int64_t q_stride, int q_heads,
-                  pivot_dtype dt, const void* out) {
+                  pivot_dtype dt, const void* out, const float* lse) {
   const int64_t esz = dt == PIVOT_BF16 ? 2 : 4, row = (int64_t)q_heads * c.d;
-  const char *q0 = static_cast<const char*>(q), *o0 = static_cast<const char*>(out);
-  return o0 < q0 + ((s.rows - 1) * q_stride + row) * esz && q0 < o0 + s.rows * row * esz;
+  const int64_t q_bytes = ((s.rows - 1) * q_stride + row) * esz, out_bytes = s.rows * row * esz;
+  const int64_t lse_bytes = s.rows * q_heads * (int64_t)sizeof(float);
+  auto meet = [](const void* a, int64_t na, const void* b, int64_t nb) {
+    const char *p = static_cast<const char*>(a), *r = static_cast<const char*>(b);
+    return p < r + nb && r < p + na;
+  };
+  return meet(out, out_bytes, q, q_bytes) ||
+         (lse && (meet(lse, lse_bytes, q, q_bytes) || meet(lse, lse_bytes, out, out_bytes)));
 }
 
 KvCache device_cache(const pivot_kv_cache& c) {
@@ -199,7 +206,7 @@ pivot_status pivot_kv_attention(const pivot_kv_cache* cache, const pivot_kv_step
   a.window = std::min(window, kFar);
   a.sinks = std::min(sinks, kFar);
   if (step->rows == 0) return PIVOT_OK;
-  if (out_overlaps(*cache, *step, q, q_stride, q_heads, dt, out)) return PIVOT_ERR_INVALID_ARG;
+  if (out_overlaps(*cache, *step, q, q_stride, q_heads, dt, out, lse_opt)) return PIVOT_ERR_INVALID_ARG;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (many_rows(step->rows, step->B, q_heads, cache->kv_heads, cache->d, dt) &&
@@ -232,7 +239,7 @@ pivot_status pivot_kv_attention_selected(const pivot_kv_cache* cache, const pivo
   a.idx_stride = index_stride;
   a.topk = topk;
   if (step->rows == 0) return PIVOT_OK;
-  if (out_overlaps(*cache, *step, q, q_stride, q_heads, dt, out)) return PIVOT_ERR_INVALID_ARG;
+  if (out_overlaps(*cache, *step, q, q_stride, q_heads, dt, out, lse_opt)) return PIVOT_ERR_INVALID_ARG;
   const cudaError_t e = launch_kv_attn(a, sms(), ws, nullptr, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? PIVOT_OK : record_cuda_error(e, "kv selected attention kernel");
 }
