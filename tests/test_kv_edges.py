@@ -260,3 +260,18 @@ def test_attention_refuses_a_log_sum_over_the_queries_or_the_outputs(call):
         assert run(lib, A.cache(), A.step(), q=A.PTR, out=A.PTR + rows, lse=lse) == 1, lse - A.PTR
     for lse in (far - 3 * 8 * 4 + 4, far - 4, far + rows - 4):
         assert run(lib, A.cache(), A.step(), q=A.PTR, out=far, lse=lse) == 1, lse - far
+
+
+def test_the_largest_cache_that_is_documented_is_taken():
+    """num_pages * kv_heads * page_size up to 2^31 - 1, for a page size that does not divide 2^31 too."""
+    import test_kv_abi as A
+
+    lib = P.lib()
+    for page, heads, pages in ((48, 1, 44_739_242), (16, 1, 134_217_727), (64, 7, 4_793_490), (48, 5, 8_947_848)):
+        slots = page * heads * pages
+        assert slots < 2 ** 31 <= slots + page * heads
+        for more, want in ((0, 0), (1, 2)):
+            c = A.cache(page_size=page, kv_heads=heads, num_pages=pages + more)
+            none = A.step(rows=0)
+            assert A.attend(lib, c, none, hq=heads, qs=1024) == want
+            assert A.append(lib, c, none, ks=1024, vs=1024, n_pos=4 * page) == want

@@ -20,7 +20,7 @@ pivot_status check_cache(const pivot_kv_cache* c) {
     return PIVOT_ERR_INVALID_ARG;
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return PIVOT_ERR_INVALID_ARG;
   if ((c->d != 64 && c->d != 128) || c->kv_heads > 1024) return PIVOT_ERR_UNSUPPORTED_SHAPE;
-  if ((int64_t)c->num_pages * c->kv_heads >= (int64_t)0x80000000ll / c->page_size) return PIVOT_ERR_UNSUPPORTED_SHAPE;
+  if ((int64_t)c->num_pages * c->kv_heads > (int64_t)0x7FFFFFFFll / c->page_size) return PIVOT_ERR_UNSUPPORTED_SHAPE;
   return PIVOT_OK;
 }
 
