@@ -68,6 +68,80 @@ def test_append_rotated_keys_that_are_not_finite_or_leave_fp32(dtype, interleave
     append_bit_for_bit(x, torch.full_like(cos, 1.5), torch.full_like(sin, 1.5), interleaved, rot)
 
 
+@gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("d,rot", [(64, 64), (128, 128), (128, 48)])
+def test_append_rotated_payload_is_the_exact_value_rounded_once(d, rot, dtype, interleaved):
+    x = torch.randn((400, 3, d), device="cuda", generator=gen(5))
+    x *= torch.exp2(torch.randint(-9, 9, (400, 1, 1), device="cuda", generator=gen(6)).float())
+    append_bit_for_bit(x.to(dtype), *angles(26 * 16, rot, 0.3), interleaved, rot)
+
+
+def beside(points, rng, dtype):
+    """(a, b, c, s) with a c - b s just beside each of the points, on both sides: a and b of the rows' type."""
+    a, b = (torch.from_numpy(rng.uniform(1, 2, points.shape) * np.abs(points) * f).to(dtype).double().numpy()
+            for f in (1.0, 0.7))
+    c = rng.uniform(0.3, 1.0, points.shape).astype(np.float32).astype(float)
+    s = ((a * c - points) / b).astype(np.float32).astype(float)
+    y = a * c - b * s
+    s = np.where(np.abs(y - points) < 2.0 ** -45 * np.abs(points), np.nextafter(s.astype(np.float32), np.float32(9)), s)
+    return a, b, c, s
+
+
+def in_fp32(a, b, c, s):
+    """The same in plain fp32: product, product, sum; and with the second product fused into the sum."""
+    f = np.float32
+    p = (a.astype(f) * c.astype(f)).astype(f)
+    return p - (b.astype(f) * s.astype(f)).astype(f), (p.astype(float) - b * s).astype(f)
+
+
+@gpu
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_rotated_values_beside_e4m3_ties_fall_as_the_exact_ones(dtype, interleaved):
+    """Rotated values so near to the middle between two e4m3 values that fp32 arithmetic lands on it or behind it."""
+    rng = np.random.default_rng(3)
+    n, half = 512, 32
+    ties = (rng.integers(8, 16, (n, half)) + 0.5) / 8 * 2.0 ** rng.integers(-4, 5, (n, half))
+    a, b, c, s = beside(ties, rng, dtype)
+    a[:, -1], b[:, -1], c[:, -1], s[:, -1] = 448.0, 0.0, 1.0, 0.0  # every block's exponent is 0
+    exact = a * c - b * s
+    wrong = [(R.round_e4m3(y.astype(float)) != R.round_e4m3(exact))[:, :-1].mean() for y in in_fp32(a, b, c, s)]
+    assert min(wrong) > 0.05  # what this test is for
+    x = np.zeros((n, 1, 64))
+    i = np.arange(half)
+    x[:, 0, 2 * i if interleaved else i], x[:, 0, 2 * i + 1 if interleaved else i + half] = a, b
+    cos, sin = np.ones((n + 16, half)), np.zeros((n + 16, half))
+    cos[:n], sin[:n] = c, s
+    cache = append_bit_for_bit(torch.from_numpy(x).cuda().to(dtype), torch.from_numpy(cos).float().cuda(),
+                               torch.from_numpy(sin).float().cuda(), interleaved, 64)
+    assert int((cache.k_exp == 0).sum()) >= n // 16
+
+
+@gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_exponent_of_rotated_values_beside_a_step(dtype):
+    """Largest values so near to 448 * 2^e, on either side, that fp32 arithmetic cannot tell."""
+    rng = np.random.default_rng(4)
+    steps = 448.0 * 2.0 ** rng.integers(-20, 20, 256)
+    a, b, c, s = beside(steps, rng, dtype)
+    exact = a * c - b * s
+    assert min(((y > steps) != (exact > steps)).mean() for y in in_fp32(a, b, c, s)) > 0.05
+    n = 16 * len(steps)  # a block for each
+    x = np.zeros((n, 1, 64))
+    cos, sin = np.ones((n + 16, 32)), np.zeros((n + 16, 32))
+    at = 16 * np.arange(len(steps)) + rng.integers(0, 16, len(steps))
+    x[at, 0, 3], x[at, 0, 35], cos[at, 3] = a, b, c
+    sin[at, 3] = s
+    # the pair's other value must not be the larger one: its sign and size come from b c + a s
+    small = np.abs(b * c + a * s) < 0.9 * steps
+    x[at[~small]] = 0.0
+    assert small.sum() > 40
+    append_bit_for_bit(torch.from_numpy(x).cuda().to(dtype), torch.from_numpy(cos).float().cuda(),
+                       torch.from_numpy(sin).float().cuda(), False, 64)
+
+
 # ---------------------------------------------------------------- attention of many rows: waits that run out
 
 
@@ -275,3 +349,62 @@ def test_the_largest_cache_that_is_documented_is_taken():
             none = A.step(rows=0)
             assert A.attend(lib, c, none, hq=heads, qs=1024) == want
             assert A.append(lib, c, none, ks=1024, vs=1024, n_pos=4 * page) == want
+
+
+# ---------------------------------------------------------------- attention: the precision that pivot.h states
+
+
+def check_stated_precision(q, cache, table, off, lens, out, query=0.0, indices=None):
+    """out of a bf16 call against the definition, with the bounds that pivot.h states and no more: scores in fp32 (d
+    products, (d + 8) 2^-24 of sum |q k|; `query` times the row's largest |q| for each element where the query is held
+    in two parts), weights rounded to fp16 (2^-11, and 2^-25 of the row's largest p 2^e), fp32 sums, bf16 outputs."""
+    d, group = cache.d, q.shape[1] // cache.kv_heads
+    pay = {n: host(getattr(cache, n)) for n in "kv"}
+    exp = {n: getattr(cache, n + "_exp").cpu().numpy().astype(float) for n in "kv"}
+    tab, x, got, scale = table.cpu().numpy(), host(q), host(out), cache.d ** -0.5
+    for r, b, p in R.rows_of(off.cpu().tolist(), lens.cpu().tolist(), q.shape[0]):
+        s = np.arange(p + 1) if indices is None else indices[r].cpu().numpy().astype(np.int64)
+        s = s[(s >= 0) & (s <= p)]
+        pg, at = tab[b, s // cache.page_size], s % cache.page_size
+        for j in range(q.shape[1]):
+            h = j // group
+            k = pay["k"][pg, h, at] * 2.0 ** exp["k"][pg, h, at // 16][:, None]
+            e = 2.0 ** exp["v"][pg, h, at // 16][:, None]
+            v = pay["v"][pg, h, at]
+            z = k @ x[r, j] * scale
+            w = np.exp(z - z.max())[:, None]
+            total = w.sum()
+            want = (w * e * v).sum(0) / total
+            dz = (np.abs(k) @ np.abs(x[r, j])).max() * (d + 8) * 2.0 ** -24 * scale
+            dz += query * np.abs(x[r, j]).max() * np.abs(k).sum(1).max() * scale
+            size = (w * e * np.abs(v)).sum(0) / total
+            far = 2.0 ** -25 * (w * e).max() * np.abs(v).sum(0) / total
+            tol = (2 * dz + 2.0 ** -11 + (len(s) + 16) * 2.0 ** -24) * size + far + 2.0 ** -8 * np.abs(want) * 1.01
+            worst = (np.abs(got[r, j] - want) / tol).max()
+            assert worst <= 1, f"row {r} head {j}: {worst:.3g} of the bound"
+
+
+@gpu
+@pytest.mark.parametrize("outlier", [1.0, 2.0 ** 11])
+@pytest.mark.parametrize("form", ["d 64", "d 128", "selected", "many rows"])
+def test_attention_of_bf16_keeps_the_stated_precision(form, outlier):
+    """Weights over many orders; and queries whose largest element, met by keys of 0, is 2^11 times the others: one fp16
+    holds all of such a query, two e4m3 parts (many rows) hold 2^-17 of its largest."""
+    d, hk, group, many = 64 if form == "d 64" else 128, 2, 4, form == "many rows"
+    lens, new = [700, 90], [40, 40] if many else [2, 2]
+    table, off, ln, pages = (wide_step if many else lambda l, n, _hq, _hk, page, seed: make_step(l, n, page, seed))(
+        lens, new, hk * group, hk, 32, 1)
+    cache = make_cache(pages, hk, 32, d, 2)
+    cache.v_exp.copy_(torch.randint(-14, 1, cache.v_exp.shape, device="cuda", generator=gen(6)).to(torch.int8))
+    k = cache.k.float()
+    k[..., 5] = 0
+    cache.k.copy_(k.to(cache.k.dtype))
+    q = make_q(sum(new), hk * group, d, "bf16", 3, 5.0)
+    q[..., 5] = 5.0 * outlier
+    idx = None
+    if form == "selected":
+        idx = torch.randint(0, 700, (sum(new), 300), dtype=torch.int32, device="cuda", generator=gen(5))
+        out, _ = P.kv_attention_selected(q, cache, idx, table, off, ln)
+    else:
+        out, _ = P.kv_attention(q, cache, table, off, ln)
+    check_stated_precision(q, cache, table, off, ln, out, 2.0 ** -17 if many else 0.0, idx)
