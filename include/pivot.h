@@ -354,8 +354,8 @@ typedef struct {
  * or (2i, 2i + 1) with `interleaved`, become (x1 cos - x2 sin, x2 cos + x1 sin).  rot is a multiple of 16, at
  * most d (0: no rotation, cos and sin NULL); n_pos >= table_width * page_size; cos and sin 16-byte aligned.
  * q [rows, q_heads, d] (optional) is rotated the same way into q_out [rows, q_heads, d] (dt), which may be q
- * itself (then with the same stride) and else shares no element with it.  Rows of positions behind the table's
- * width keep their q_out as it was.
+ * itself (then with the same stride) and else shares no element with it; it shares none with k or v, and the cache's
+ * four arrays share none with one another.  Rows of positions behind the table's width keep their q_out as it was.
  *
  * The scale of a block whose first token of the sequence is new: the least e in [PIVOT_KV_EXP_MIN,
  * PIVOT_KV_EXP_MAX] with |y| <= 448 * 2^e for the finite values y of its new tokens and head.  A block that
@@ -363,8 +363,9 @@ typedef struct {
  * the earlier payload is rounded again to the new scale (exact, but for values that fall below e4m3's normal
  * range).  payload = e4m3(y * 2^-e), to nearest even; NaN stays NaN, larger values and infinities become
  * +-448.  Nothing else of the cache is written.  Two sequences may share a page only where neither appends to it.
- * fp32 arithmetic (the rotation's products and one sum); an exponent is exact: a largest value within rounding of
- * a step between two exponents is computed again in 64 bits.
+ * A rotated key is rounded once: the sum keeps its products' errors and is rounded to odd at 24 bits, so that scale and
+ * payload are those of the exact value, beside a tie and beside a step between two exponents too.  A finite value that no
+ * fp32 holds is finite here.  q is rotated in plain fp32 (two products and their sum) and then rounded to dt.
  * Errors: PIVOT_ERR_INVALID_ARG, PIVOT_ERR_UNSUPPORTED_SHAPE, PIVOT_ERR_CUDA. */
 PIVOT_API pivot_status pivot_kv_append(const pivot_kv_cache *cache, const pivot_kv_step *step, const void *k,
                                        int64_t k_stride, const void *v, int64_t v_stride, pivot_dtype dt,
@@ -379,7 +380,12 @@ PIVOT_API pivot_status pivot_kv_append(const pivot_kv_cache *cache, const pivot_
  * that sees nothing gives zeros and lse -inf.  What absent or masked positions hold, NaN included, changes nothing.
  * Scores, softmax statistics and output sums are fp32.  bf16: the weights p enter the output product with 8 bits
  * or more, fp32 with 21 or more; where p 2^e (e the value's exponent) lies under 2^-19 (fp32: 2^-17) of the row's
- * largest, with an error of at most 2^-25 (fp32: 2^-38) of that.
+ * largest, with an error of at most 2^-25 (fp32: 2^-38) of that.  A query's elements enter
+ * the scores with an error of at most 2^-39 of the row's largest (bf16: exactly, down to 2^-31 of it), but for one kind
+ * of call: many bf16 rows of d = 128 (more than 16 query rows for a key head and sequence on average, and work that
+ * repays it) may be multiplied as two e4m3 parts, with an error of at most 2^-17 of the row's largest (exactly, down to
+ * 2^-9 of it).  Such a call whose masked places hold NaN values, or that reads values with exponents above 16, is
+ * computed twice, and takes several times as long.
  * The same call gives the same bits every time.  out, lse_opt and q must not overlap.
  * ws: pivot_kv_workspace_size bytes on the current device (256-byte aligned; 0: the call would be refused), with
  * topk 0 for pivot_kv_attention.  pivot_last_device_status reads it: a wait that ran out is reported there, and the

@@ -694,9 +694,10 @@ def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None,
     k, v [rows, kv_heads, d] (bf16 or fp32; rows may be slices of a wider tensor).  Sequence b owns rows
     row_offsets[b] .. row_offsets[b+1]-1, the last of its lens[b] tokens (this step's included), and its
     position s lies in page block_table[b, s // page_size].  row_offsets [B+1] and lens [B]: int64 CUDA
-    tensors, DeviceOffsets, or host values (copied on every call).  cos, sin [positions, rot / 2] fp32
-    (positions >= width * page_size) rotate the first rot dims of k, and of q [rows, heads, d] into q_out (a new tensor unless given; q
-    itself is allowed): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no
+    tensors, DeviceOffsets, or host values (copied on every call; a captured call keeps those it was captured
+    with).  cos, sin [positions, rot / 2] fp32 (positions >= width * page_size) rotate the first rot dims of k, and of
+    q [rows, heads, d] into q_out (a new tensor unless given; q itself is allowed, else it shares no memory with k, v
+    or q): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no
     token, or lie behind the table's width, leave cache and q_out as they were.  There is no backward pass: k, v or q
     that require a gradient are refused where gradients are on."""
     other = _kv_elsewhere(cache, stream)
@@ -790,9 +791,9 @@ def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Op
 
     q [rows, heads, d] (bf16 or fp32), heads a multiple of the cache's; the step as kv_append takes it,
     after it.  The row at position p sees the positions s <= p; with ``window`` only s > p - window, and the
-    first ``sinks``.  ``scale`` defaults to d ** -0.5.  ``out`` must not share memory with q.  ``ws``: scratch kept
-    between calls, which must then be ordered (last_device_status reads it); else each call has its own.  ``lse``: False, True, or an fp32 [rows, heads] tensor
-    that receives ln sum exp(scale q.k).  Rows that see nothing give zeros and -inf; rows behind
+    first ``sinks``.  ``scale`` defaults to d ** -0.5.  ``out``, ``lse`` and q must not share memory.  ``ws``: scratch
+    kept between calls, which must then be ordered (last_device_status reads it); else each call has its own.
+    ``lse``: False, True, or an fp32 [rows, heads] tensor that receives ln sum exp(scale q.k).  Rows that see nothing give zeros and -inf; rows behind
     row_offsets[B] are not written (they are undefined in an ``out`` that the call allocates).  There is no backward
     pass: a q that requires a gradient is refused where gradients are on."""
     other = _kv_elsewhere(cache, stream)
@@ -809,8 +810,8 @@ def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Op
         w = _kv_scratch(rows, step.B, heads, cache, 0, dt, ws, "pivot_kv_attention")
         _check(lib().pivot_kv_attention(
             cache._ref, ctypes.byref(step), q.data_ptr(), qs, heads, dt, d ** -0.5 if scale is None else scale,
-            min(window, _FAR), min(sinks, _FAR), out.data_ptr(), None if lse is None else lse.data_ptr(), w.data_ptr(), w.numel(),
-            _raw_stream(cache.device.index)), "pivot_kv_attention")
+            min(window, _FAR), min(sinks, _FAR), out.data_ptr(), None if lse is None else lse.data_ptr(), w.data_ptr(),
+            w.numel(), _raw_stream(cache.device.index)), "pivot_kv_attention")
     return out, lse
 
 

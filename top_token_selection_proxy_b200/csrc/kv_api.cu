@@ -101,7 +101,9 @@ bool many_rows(int64_t rows, int B, int q_heads, int kv_heads, int d, pivot_dtyp
 // needs some 14 us more for its launches and first tiles, and takes a tile of 128 rows in the time of about 1.5 of 16.
 // Measured (16 against 128 rows an item, us): 1 sequence of 4000, 8 key heads of 64 rows (1024) 32 against 41, of 128
 // rows (2048) 43 against 41; 16 of 500, 4 heads of 24 rows (512) 26 against 29; 16 of 4000, 4 heads of 20 rows (4096)
-// 63 against 50; 16 of 32000, 2 heads of 64 rows (32000) 395 against 114.
+// 63 against 50; 16 of 32000, 2 heads of 64 rows (32000) 395 against 114.  These are batches of equal sequences under
+// tables of their length, and the rule knows no others: with a wider table, or one long sequence among short ones, the
+// call as a whole still goes one way, and may pay those 14 us, or take many rows 16 at a time.
 bool much_work(const pivot_kv_cache& c, const pivot_kv_step& s, int q_heads, int64_t window, int64_t sinks) {
   const int64_t group = q_heads / c.kv_heads, cap = (int64_t)s.table_width * c.page_size;
   int64_t seen = cap;

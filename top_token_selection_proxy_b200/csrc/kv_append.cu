@@ -8,11 +8,12 @@
 //
 // What bounds it: bytes (a key row is read once at 2 or 4 bytes an element and written at 1, a query row is read
 // and written).  A block is two warps' work for one head and one of k and v: its (up to 16) token rows stay in
-// registers between the maximum and the rounding, so nothing is read twice; 8 elements a lane, 16-byte loads.
+// registers between the maximum and the rounding, so nothing is read twice; 8 elements a lane, 16-byte loads.  (A block
+// that holds something not finite is read and rotated once more, with fp64 where fp32 gives no number.)
 // Query rows are other CTAs' work: a warp keeps a row's angles and takes its heads in batches of loads.
 //
-// Measured: a prompt of 8192 tokens, 8 key heads and 64 query heads of 128, bf16: 79 us, 4.1 TB/s (62 % of the measured
-// copy bandwidth); 9 prompts of up to 1900 tokens, 24 and 3 heads, together: 27 us (50 %); one token for each of 32
+// Measured: a prompt of 8192 tokens, 8 key heads and 64 query heads of 128, bf16: 80 us, 4.0 TB/s (61 % of the measured
+// copy bandwidth); 9 prompts of up to 1900 tokens, 24 and 3 heads, together: 27 us (49 %); one token for each of 32
 // sequences: 5 us on the GPU, which is latency.  The next bound is the issue slots (53 % of their peak): the keys'
 // two-float rotation takes some 15 operations an element, where a plain fp32 one would now and then land on the wrong
 // side of an e4m3 tie.
@@ -140,7 +141,8 @@ struct Turned {
 
 // a c + b s rounded to odd at 24 bits: the exact value's neighbour whose last bit is set, unless it is exact.  A
 // later rounding to fewer bits, and a comparison with a power of two times 448, then give what the exact value
-// gives.  The products' and the sum's own errors are exact fp32 values (fused multiply-add; Knuth's two-sum).
+// gives.  The products' and the sum's own errors are exact fp32 values (fused multiply-add; Knuth's two-sum); their sum
+// is rounded, so a remainder under 2^-47 of the terms may not show in the last bit (2 of 2e8 random rotations).
 struct TurnedOdd {
   __device__ float operator()(float a, float c, float b, float s) const {
     const float p = __fmul_rn(a, c), q = __fmul_rn(b, s);

@@ -5,7 +5,8 @@
 // A key is payload * 2^e with one e for 16 tokens and head, so z = (q . payload) * 2^e scale2, and the output sum
 // takes weights p * 2^e.  Both sums are kept relative to a reference u of each row, a value of z + e that may lag
 // behind the largest by as much as fp16 holds: weights enter the product as fp16 values of 2^(z + e - u + 2), the
-// denominator adds 2^(z - u) in fp32, which holds it for all scales there are (|e| <= 60).
+// denominator adds 2^(z - u) in fp32, which holds it for all scales there are (|e| <= 60).  fp16 keeps 11 bits of a weight
+// where a bf16 output keeps 8 of their sum; fp32 calls multiply what it leaves as a second fp16 (21 bits), a second product.
 //
 // What bounds it: the cache's bytes (2 d and a little for each token and key head, read once for up to 16 query
 // rows).  So the payload goes to registers in the order in which the matrix instruction wants it, without a
@@ -19,11 +20,11 @@
 // stretch of it.  A stretch that begins or ends inside an item leaves a partial result, which kv_merge_kernel joins in
 // a fixed order.  (The places: 48 sequences of 1 to 32768 tokens, window 1024, d = 64: 60 us without them, 35 us with.)
 //
-// Measured: 16 sequences of 32000 tokens, 8 key heads, one row of 8 query heads each: d = 128 bf16 251 us (4.17 TB/s,
-// 64 % of the measured copy bandwidth), fp32 337 us; d = 64 129 us (62 %).  1 of 200000: 110 us (57 %).  Not DRAM but
+// Measured: 16 sequences of 32000 tokens, 8 key heads, one row of 8 query heads each: d = 128 bf16 251 us (4.19 TB/s,
+// 64 % of the measured copy bandwidth), fp32 339 us; d = 64 130 us (62 %).  1 of 200000: 109 us (57 %).  Not DRAM but
 // the warps' own latency holds it there (few warps fit beside the registers that the sums take; 25 % of the tensor
 // pipe's cycles): conversions to fp16, exponentials and products follow one another within a warp.  Selected rows (1024
-// rows of 64 query heads over 2048 tokens each): 480 us; each of the 4 groups of 16 heads gathers the list for itself,
+// rows of 64 query heads over 2048 tokens each): 484 us; each of the 4 groups of 16 heads gathers the list for itself,
 // from L2.
 #include <type_traits>
 

@@ -4,7 +4,8 @@
 // The same sums as kv_attention.cu, for items of 128 query rows by tiles of 128 tokens:
 //   S = Q K^T   kind::f8f6f4.  Keys are multiplied as they lie in the cache: TMA brings e4m3 pages into the swizzled
 //               operand layout, nothing is converted.  A bf16 query has 8 bits: two e4m3 parts of 4 bits hold it
-//               (scaled to 2^8; what lies 2^-10 below a row's largest keeps fewer), two products into one sum.
+//               (scaled to [2^7, 2^8); what lies 2^-9 below a row's largest keeps fewer, and is off by up to 2^-17 of
+//               that largest), two products into one sum.
 //   O += P V    kind::f16.  Weights leave the softmax as fp16 and stay in tensor memory; four warps turn the values
 //               into fp16 (an e4m3 product would leave the weights 4 bits).
 // Two tiles are in work at a time, each with its own S, P and softmax warpgroup, into one O: while one is in the
@@ -14,9 +15,9 @@
 //
 // What bounds it: for full items the softmax (a tile's 128 x 128 exponentials are 1024 clocks of an SM, its products
 // 1060, and what else the softmax warps issue comes on top); with half the rows or fewer the cache's bytes.
-// Measured: rows 4096 .. 8191 of a prompt, 32 query and 4 key heads: 547 us, 753 TFLOP/s of the 4 d a visible pair
-// (46 % of the measured bf16 burst).  32 sequences of 16000 to 200000 tokens, 4 rows of 32 heads on 2: 600 us, 3.2 TB/s
-// (48 %), where kv_attention.cu takes 3600.  Four softmax warpgroups, each with half the registers, took 995 and 714 us
+// Measured: rows 4096 .. 8191 of a prompt, 32 query and 4 key heads: 552 us, 746 TFLOP/s of the 4 d a visible pair
+// (46 % of the measured bf16 burst).  32 sequences of 16000 to 200000 tokens, 4 rows of 32 heads on 2: 616 us, 3.1 TB/s
+// (47 %; 592 to 630 us from one B200 to the next), where kv_attention.cu takes 3600.  Four softmax warpgroups, each with half the registers, took 995 and 714 us
 // where two took 662 and 611; loops unrolled (past the instruction cache) twice as long.
 #include <type_traits>
 
