@@ -205,11 +205,13 @@ def test_the_largest_window_is_no_window(dtype):
 def test_a_cache_keeps_the_tensors_that_its_calls_write():
     """The calls go by pointers taken once: an attribute that pointed elsewhere would not be what they write."""
     cache = P.KVCache.__new__(P.KVCache)
-    for name in ("k", "v", "k_exp", "v_exp", "device", "num_pages", "kv_heads", "page_size", "d", "_c", "_ref", "x"):
+    for name in ("k", "v", "k_exp", "v_exp", "device", "num_pages", "kv_heads", "page_size", "d", "_c", "_ref"):
         with pytest.raises(AttributeError):
             setattr(cache, name, torch.zeros(1))
         with pytest.raises(AttributeError):
             delattr(cache, name)
+    cache.owner = "a caller's own attribute"
+    assert cache.owner and not hasattr(cache, "k")
 
 
 @gpu

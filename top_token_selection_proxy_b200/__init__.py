@@ -599,8 +599,7 @@ class KVCache:
     references to them and the calls below write them in place, where they lay when the cache was made: its
     attributes are fixed, and the tensors' storage must stay.  ``KVCache.empty`` allocates them."""
 
-    __slots__ = ("k", "v", "k_exp", "v_exp", "device", "num_pages", "kv_heads", "page_size", "d", "_c", "_ref",
-                 "__weakref__")
+    _FIXED = ("k", "v", "k_exp", "v_exp", "device", "num_pages", "kv_heads", "page_size", "d", "_c", "_ref")
 
     def __init__(self, k, v, k_exp, v_exp):
         if k.dim() != 4 or k.dtype != torch.float8_e4m3fn or v.dtype != torch.float8_e4m3fn:
@@ -616,15 +615,18 @@ class KVCache:
         if len({t.device for t in (k, v, k_exp, v_exp)}) != 1:
             raise ValueError("k, v, k_exp and v_exp must be on one device")
         c = _CacheC(k.data_ptr(), v.data_ptr(), k_exp.data_ptr(), v_exp.data_ptr(), pages, heads, page, d)
-        for name, value in zip(self.__slots__, (k, v, k_exp, v_exp, k.device, pages, heads, page, d, c,
-                                                ctypes.byref(c))):
-            object.__setattr__(self, name, value)
+        self.__dict__.update(zip(self._FIXED, (k, v, k_exp, v_exp, k.device, pages, heads, page, d, c,
+                                               ctypes.byref(c))))
 
-    def __setattr__(self, name, value):  # the C struct would go on pointing at what was there
-        raise AttributeError(f"a KVCache's {name} cannot be changed; make another KVCache")
+    def __setattr__(self, name, value):
+        if name in self._FIXED:  # the C struct would go on pointing at what was there
+            raise AttributeError(f"a KVCache's {name} cannot be changed; make another KVCache")
+        object.__setattr__(self, name, value)
 
     def __delattr__(self, name):
-        self.__setattr__(name, None)
+        if name in self._FIXED:
+            raise AttributeError(f"a KVCache's {name} cannot be removed")
+        object.__delattr__(self, name)
 
     @classmethod
     def empty(cls, num_pages: int, kv_heads: int, page_size: int, d: int, device="cuda") -> "KVCache":
