@@ -14,7 +14,7 @@
 //
 // Measured: a prompt of 8192 tokens, 8 key heads and 64 query heads of 128, bf16: 80 us, 4.0 TB/s (61 % of the measured
 // copy bandwidth); 9 prompts of up to 1900 tokens, 24 and 3 heads, together: 27 us (49 %); one token for each of 32
-// sequences: 5 us on the GPU, which is latency.  The next bound is the issue slots (53 % of their peak): the keys'
+// sequences: 5 us on the GPU, which is latency.  The next bound is the issue slots (47 to 53 % of their peak): the keys'
 // two-float rotation takes some 15 operations an element, where a plain fp32 one would now and then land on the wrong
 // side of an e4m3 tie.
 #include "kv.cuh"
