@@ -380,12 +380,12 @@ PIVOT_API pivot_status pivot_kv_append(const pivot_kv_cache *cache, const pivot_
  * that sees nothing gives zeros and lse -inf.  What absent or masked positions hold, NaN included, changes nothing.
  * Scores, softmax statistics and output sums are fp32.  bf16: the weights p enter the output product with 8 bits
  * or more, fp32 with 21 or more; where p 2^e (e the value's exponent) lies under 2^-19 (fp32: 2^-17) of the row's
- * largest, with an error of at most 2^-25 (fp32: 2^-38) of that.  A query's elements enter
- * the scores with an error of at most 2^-39 of the row's largest (bf16: exactly, down to 2^-31 of it), but for one kind
- * of call: many bf16 rows of d = 128 (more than 16 query rows for a key head and sequence on average, and work that
- * repays it) may be multiplied as two e4m3 parts, with an error of at most 2^-17 of the row's largest (exactly, down to
- * 2^-9 of it).  Such a call whose masked places hold NaN values, or that reads values with exponents above 16, is
- * computed twice, and takes several times as long.
+ * largest, with an error of at most 2^-25 (fp32: 2^-38) of that.  A query's elements enter the scores with an error of
+ * at most 2^-39 of the row's largest (bf16: exactly, down to 2^-31 of it), but for one kind of call: many bf16 rows of
+ * d = 128 (more than 16 query rows for a key head and sequence on average, and work that repays it) may be multiplied as
+ * two e4m3 parts, with an error of at most 2^-17 of the row's largest (exactly, down to 2^-9 of it).  Such a call whose
+ * masked places hold NaN values, or that reads values with exponents above 16, is computed twice, and takes several times
+ * as long.
  * The same call gives the same bits every time.  out, lse_opt and q must not overlap.
  * ws: pivot_kv_workspace_size bytes on the current device (256-byte aligned; 0: the call would be refused), with
  * topk 0 for pivot_kv_attention.  pivot_last_device_status reads it: a wait that ran out is reported there, and the

@@ -699,9 +699,9 @@ def kv_append(cache: KVCache, k, v, block_table, row_offsets, lens, *, cos=None,
     tensors, DeviceOffsets, or host values (copied on every call; a captured call keeps those it was captured
     with).  cos, sin [positions, rot / 2] fp32 (positions >= width * page_size) rotate the first rot dims of k, and of
     q [rows, heads, d] into q_out (a new tensor unless given; q itself is allowed, else it shares no memory with k, v
-    or q): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no
-    token, or lie behind the table's width, leave cache and q_out as they were.  There is no backward pass: k, v or q
-    that require a gradient are refused where gradients are on."""
+    or q): pairs (i, i + rot/2), or (2i, 2i + 1) with ``interleaved``.  Rows that belong to no token, or lie behind the
+    table's width, leave cache and q_out as they were.  There is no backward pass: k, v or q that require a gradient
+    are refused where gradients are on."""
     other = _kv_elsewhere(cache, stream)
     if other is not None:
         with torch.cuda.stream(other):
@@ -795,9 +795,9 @@ def kv_attention(q, cache: KVCache, block_table, row_offsets, lens, *, scale: Op
     after it.  The row at position p sees the positions s <= p; with ``window`` only s > p - window, and the
     first ``sinks``.  ``scale`` defaults to d ** -0.5.  ``out``, ``lse`` and q must not share memory.  ``ws``: scratch
     kept between calls, which must then be ordered (last_device_status reads it); else each call has its own.
-    ``lse``: False, True, or an fp32 [rows, heads] tensor that receives ln sum exp(scale q.k).  Rows that see nothing give zeros and -inf; rows behind
-    row_offsets[B] are not written (they are undefined in an ``out`` that the call allocates).  There is no backward
-    pass: a q that requires a gradient is refused where gradients are on."""
+    ``lse``: False, True, or an fp32 [rows, heads] tensor that receives ln sum exp(scale q.k).  Rows that see nothing
+    give zeros and -inf; rows behind row_offsets[B] are not written (they are undefined in an ``out`` that the call
+    allocates).  There is no backward pass: a q that requires a gradient is refused where gradients are on."""
     other = _kv_elsewhere(cache, stream)
     if other is not None:
         with torch.cuda.stream(other):

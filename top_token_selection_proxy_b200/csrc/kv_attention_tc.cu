@@ -17,8 +17,9 @@
 // 1060, and what else the softmax warps issue comes on top); with half the rows or fewer the cache's bytes.
 // Measured: rows 4096 .. 8191 of a prompt, 32 query and 4 key heads: 552 us, 746 TFLOP/s of the 4 d a visible pair
 // (46 % of the measured bf16 burst).  32 sequences of 16000 to 200000 tokens, 4 rows of 32 heads on 2: 616 us, 3.1 TB/s
-// (47 %; 592 to 630 us from one B200 to the next), where kv_attention.cu takes 3600.  Four softmax warpgroups, each with half the registers, took 995 and 714 us
-// where two took 662 and 611; loops unrolled (past the instruction cache) twice as long.
+// (47 %; 592 to 630 us from one B200 to the next), where kv_attention.cu takes 3600.  Four softmax warpgroups, each with
+// half the registers, took 995 and 714 us where two took 662 and 611; loops unrolled (past the instruction cache) twice as
+// long.
 #include <type_traits>
 
 #include "kv.cuh"
@@ -630,8 +631,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         // compiler masks every tile.)
         // This tile's first weights, times f: a power of two, so that no weight is rounded twice (a factor of 11 bits put all
         // of a tile's weights off by up to 2^-12 together).  One below fp16's normal range is applied as two: a weight of
-        // 2^15 times it is still one that counts.  (Products in fp32 would be 64 instructions more in each of three places: the whole
-        // kernel took 18 % longer, with two factors 4 %.)
+        // 2^15 times it is still one that counts.  (Products in fp32 would be 64 instructions more in each of three places:
+        // the whole kernel took 18 % longer, with two factors 4 %.)
         auto scale_weights = [&](int columns, float f) {
           const __half2 f1 = __float2half2_rn(fmaxf(f, 0x1p-14f)), f2 = __float2half2_rn(fminf(f * 0x1p14f, 1.f));
           tmem_wait_st();
